@@ -61,7 +61,8 @@ typedef enum lsa_dtype {
 } lsa_dtype;
 
 /* Library version, major*10000 + minor*100 + patch. */
-/* sizeof(lsa_params) for which = 0, sizeof(lsa_ctx_view) for 1, else -1: lets a
+/* sizeof(lsa_params) for which = 0, sizeof(lsa_ctx_view) for 1, sizeof(lsa_page_cache)
+ * for 10, sizeof(lsa_rope) for 11, sizeof(lsa_page_table) for 12, else -1: lets a
  * binding that mirrors the structs check its layout.  Needs no GPU. */
 int64_t lsa_struct_size(int32_t which);
 int32_t lsa_version(void);
@@ -342,6 +343,196 @@ lsa_status lsa_sparse_attn(const void *Q, lsa_dtype dtype, const void *kv, int64
                            int64_t k_off, int64_t v_off, const int32_t *rows, int32_t B,
                            int32_t Hq, int32_t D, int32_t k, float scale, void *out, float *lse,
                            void *workspace, size_t ws_bytes, int32_t *err, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Paged key-value cache.
+ *
+ * Beside the sparse layers a decode step runs dense ones, whose keys and values
+ * live in pages of page_size entries.  A sequence's row of the page table names
+ * the pages that hold it: entry t (t < its length) is slot t % page_size of page
+ * table[row][t / page_size].  The operators below append a step's heads to such
+ * a cache (lsa_qk_norm_rope), attend over it (lsa_paged_attn) and keep its pages
+ * (lsa_page_grow, _fork, _free, _compact, _copy).
+ *
+ * lsa_page_cache describes the memory of one layer.  K of (page p, slot s, head
+ * h) is the D elements from k + p * page_stride + s * slot_stride + h *
+ * head_stride on (strides in elements), V likewise from v.  v == k is a latent
+ * head whose rows serve as both.  E4M3 rows have one fp32 scale each (value =
+ * code * scale), at k_scale[(p * page_size + s) * Hkv + h]; with v == k, v_scale
+ * == k_scale.
+ * Layout rules: D a multiple of 16, at most 512; k, v and every stride (in bytes)
+ * multiples of 16; a stride is at least D where its extent is above 1; n_pages *
+ * page_size < 2^31 entries are addressed by 64-bit offsets.
+ * ---------------------------------------------------------------------- */
+typedef struct lsa_page_cache {
+    void *k, *v;                /* device */
+    float *k_scale, *v_scale;   /* device [n_pages, page_size, Hkv] for E4M3, else NULL */
+    lsa_dtype dtype;            /* of the rows */
+    int32_t page_size, Hkv, D;
+    int64_t n_pages;
+    int64_t page_stride, slot_stride, head_stride;   /* elements */
+} lsa_page_cache;
+
+/* ------------------------------------------------------------------------
+ * lsa_paged_attn -- attention of one new token per sequence over a paged cache:
+ * group-query (query head j reads kv head j / (Hq / Hkv)), multi-query (Hkv = 1)
+ * or latent (v == k).
+ *
+ *   a_t = scale * Q[b,j,:] . K_t     out[b,j,:] = sum_t softmax(a)_t V_t
+ *   lse[b,j] = log sum_t exp(a_t)
+ *
+ * over the entries t of sequence b with max(0, n - window) <= t < n, n =
+ * seq_len[b] (window 0: all).  The new token's own entry is in the cache already
+ * (lsa_qk_norm_rope puts it there).  A sequence without entries, or whose scores
+ * are all -infinity, gets out = 0 and lse = -infinity.
+ *
+ * Q         [B, Hq, D]: F32 with an F32 cache, BF16 with a BF16 or E4M3 one;
+ *           sequence b starts at element b * q_stride.
+ * out       [B, Hq, D] of Q's type, contiguous.   lse  [B, Hq] fp32 or NULL.
+ * table     device int32, row b of max_pages page indices at b * table_stride.
+ * seq_len   device int32 [B].  Below 0 counts as 0; above max_pages * page_size
+ *           it is cut there and *err = LSA_ERR_CAPACITY.
+ * A page index outside [0, n_pages) leaves its entries out and *err =
+ * LSA_ERR_INVALID.  Slots at or past a sequence's length are not read.
+ * workspace at least lsa_paged_attn_workspace_size(cache, B, Hq) bytes, 16-byte
+ *           aligned; contents need not be initialised; calls that share it must
+ *           not overlap.  The size is that of the current device.
+ * err       device error word or NULL.
+ * Products and sums are held in fp32 (E4M3 rows enter exactly); each query's
+ * entries are split over the device's SMs and joined in a fixed order, so the
+ * same call gives the same bits.  One launch where a sequence's table holds few
+ * entries, else two.
+ * ---------------------------------------------------------------------- */
+size_t lsa_paged_attn_workspace_size(const lsa_page_cache *cache, int32_t B, int32_t Hq);
+lsa_status lsa_paged_attn(const void *Q, lsa_dtype q_dtype, int64_t q_stride, const lsa_page_cache *cache,
+                          const int32_t *table, int64_t table_stride, int32_t max_pages,
+                          const int32_t *seq_len, int32_t B, int32_t Hq, int32_t window, float scale,
+                          void *out, float *lse, void *workspace, size_t ws_bytes, int32_t *err,
+                          void *stream);
+
+/* ------------------------------------------------------------------------
+ * lsa_qk_norm_rope -- a step's query and key heads: a norm of each head, the
+ * rotation by position, and the append of keys and values to the paged cache, in
+ * one pass.  For every token t and head x (D elements):
+ *
+ *   y_i = x_i * w_i / sqrt(mean_j x_j^2 + eps)          (w NULL: y = x)
+ *   the pairs (a, b) of the first rot_dim elements turn by the angle
+ *   phi_i = pos[t] * freq[i]:  a' = m (a cos phi - b sin phi),
+ *                              b' = m (a sin phi + b cos phi),  m = mscale
+ *
+ * and the elements from rot_dim on stay.  Pair i is (y_i, y_{i + rot_dim/2}), or
+ * (y_{2i}, y_{2i+1}) with `interleaved`.  `inverse` turns by -phi_i: with mscale
+ * 1 it undoes the rotation, and it is the rotation's gradient.  Angles are taken
+ * in 64 bits, so far positions keep their fraction of a turn.
+ *
+ * q, k, v   [T, Hq, D], [T, Hkv, D], [T, Hkv, D] of `dtype` (F32 or BF16); token t
+ *           starts at element t * q_stride (k_stride, v_stride), so that they may
+ *           be parts of one projection's output.  k NULL: queries only.
+ * q_out, k_out  likewise; may be q and k themselves (same strides).  k_out may be
+ *           NULL where a cache takes the keys.
+ * q_weight, k_weight  [D] of `dtype`, or NULL (no norm of those heads).
+ * pos       device int32 [T], required with rot_dim > 0.
+ * rope      NULL: no rotation.  rope->freq: device fp64 [rot_dim / 2], radians per
+ *           position (lsa_rope_frequencies computes plain and scaled ones).
+ * cache     NULL, or where keys and values go: token t becomes entry at[t] of
+ *           table row seq[t] (row t if seq is NULL).  Tokens with a negative at or
+ *           seq are not appended.  v is required unless the cache is latent (v ==
+ *           k), where it must be NULL.  Rows of an E4M3 cache are rounded from
+ *           fp32 with scale = max|y| / 448 (1 for a row of zeros).  No two tokens
+ *           may name the same entry.  An entry outside the table (n_rows rows,
+ *           max_pages * page_size entries) or on a page outside [0, n_pages) is not
+ *           written and *err = LSA_ERR_INVALID.
+ * Cache types: that of `dtype`, or E4M3.  D a multiple of 16 up to 512; rot_dim
+ * even, 0 .. D; pointers and strides 16-byte multiples.  Norms and rotations are
+ * computed in fp32 and rounded once.  One launch; T = 0 launches nothing.
+ * ---------------------------------------------------------------------- */
+typedef struct lsa_rope {
+    const double *freq;     /* device [rot_dim / 2] */
+    int32_t rot_dim;
+    int32_t interleaved;
+    int32_t inverse;
+    float mscale;           /* 0 means 1 */
+} lsa_rope;
+lsa_status lsa_qk_norm_rope(const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride,
+                            const void *k, int64_t k_stride, void *k_out, int64_t k_out_stride,
+                            const void *v, int64_t v_stride, lsa_dtype dtype, int64_t T, int32_t Hq,
+                            int32_t Hkv, int32_t D, const void *q_weight, const void *k_weight,
+                            float eps, const int32_t *pos, const lsa_rope *rope,
+                            const lsa_page_cache *cache, const int32_t *table, int64_t table_stride,
+                            int32_t n_rows, int32_t max_pages, const int32_t *seq, const int32_t *at,
+                            int32_t *err, void *stream);
+
+/* Rotation frequencies, on the host (no GPU needed): freq_i for i < rot_dim / 2, and the
+ * factor mscale that goes with them.  With theta_i = base^(-2i / rot_dim) and s = factor >= 1:
+ *   PLAIN   theta_i
+ *   LINEAR  theta_i / s                          (positions squeezed into the trained range)
+ *   NTK     theta_i of base * s^(r / (r - 2)), r = rot_dim   (the lowest frequency / s, the highest kept)
+ *   YARN    theta_i (1 - g_i) + theta_i / s * g_i: g_i rises from 0 to 1, linearly in i, between the pairs that
+ *           turn beta_fast and beta_slow times over orig_len positions; mscale = 0.1 ln s + 1  (the published
+ *           method of that name)
+ * The others' mscale is 1.  Errors: LSA_ERR_INVALID for a null pointer, an odd or non-positive rot_dim, base <= 1,
+ * s < 1, NTK with rot_dim < 4, YARN without 0 < beta_slow < beta_fast and orig_len >= 1. */
+typedef enum lsa_rope_kind { LSA_ROPE_PLAIN = 0, LSA_ROPE_LINEAR = 1, LSA_ROPE_NTK = 2, LSA_ROPE_YARN = 3 } lsa_rope_kind;
+lsa_status lsa_rope_frequencies(lsa_rope_kind kind, int32_t rot_dim, double base, double factor,
+                                int64_t orig_len, double beta_fast, double beta_slow,
+                                double *freq_host, float *mscale_host);
+
+/* ------------------------------------------------------------------------
+ * The pages of a cache.  One set of books serves every layer's lsa_page_cache:
+ *   table [n_rows, max_pages]  page indices, -1 where a row holds none
+ *   len   [n_rows]             entries of each row
+ *   refs  [n_pages]            rows that hold the page; 0: free
+ * all int32 on the device, so the calls below run on the stream with the kernels
+ * that use the pages and can be captured with them.  Row r holds the first
+ * ceil(len[r] / page_size) entries of its table row.  Full pages may be shared
+ * (refs > 1); a page in part filled belongs to one row.  New pages are always the
+ * free ones of the lowest index, in the order of the call's rows: the same books
+ * give the same pages.
+ *
+ * lsa_page_grow and lsa_page_fork either do all of a call or nothing: where the pool has too few free pages or a row would pass max_pages,
+ * *err = LSA_ERR_CAPACITY; where a row index is out of range (or, for a fork, a
+ * dst row is not empty, is named twice or is a src too), *err = LSA_ERR_INVALID; and the books
+ * stay as they are (and a fork's list of copies is empty).  Page indices
+ * outside [0, n_pages) in the books are never followed.
+ * Limits: n_rows <= 65536, n_pages <= 2^24, max_pages * page_size < 2^31.  `err` may
+ * be NULL.
+ * ---------------------------------------------------------------------- */
+typedef struct lsa_page_table {
+    int32_t *table, *len, *refs;   /* device */
+    int32_t n_rows, max_pages, page_size;
+    int64_t n_pages;
+} lsa_page_table;
+
+/* Row r becomes add[r] entries longer (add: device int32 [n_rows], negative counts as 0) and takes the pages that
+ * needs; the entries themselves are the caller's to write.  One launch. */
+lsa_status lsa_page_grow(const lsa_page_table *pt, const int32_t *add, int32_t *err, void *stream);
+
+/* Row dst[i] becomes a copy of row src[i] (i < n; device int32 [n]): it shares the full pages, and for a last page in
+ * part filled it takes a new one, listed as (copy_src[i], copy_dst[i]) for lsa_page_copy on each layer's cache (-1, -1
+ * where nothing has to be copied; device int32 [n]).  dst rows are empty (len 0) and distinct; a src row may be named
+ * any number of times.  n <= n_rows.  Two launches. */
+lsa_status lsa_page_fork(const lsa_page_table *pt, const int32_t *src, const int32_t *dst, int32_t n,
+                         int32_t *copy_src, int32_t *copy_dst, int32_t *err, void *stream);
+
+/* Rows rows[0 .. n) (device int32) give back their pages and become empty.  A row named twice is freed once; a row
+ * index out of range is skipped, and a page whose count is already 0 keeps it: *err = LSA_ERR_INVALID for both.  One
+ * launch. */
+lsa_status lsa_page_free(const lsa_page_table *pt, const int32_t *rows, int32_t n, int32_t *err, void *stream);
+
+/* Packs the pool: with L pages held, those at or past index L move, in ascending order, to the free ones below L, in
+ * ascending order.  Writes the table and counts after the move to table_out [n_rows, max_pages] and refs_out [n_pages]
+ * (both may be the books' own, to pack in place), the moves to move_src / move_dst [n_pages] (-1 padded) and their
+ * number to n_moves [1], for lsa_page_copy on each layer's cache.  Afterwards pages L .. n_pages - 1 are free.
+ * workspace: lsa_page_compact_workspace_size(n_pages) bytes, 16-byte aligned.  Three launches. */
+size_t lsa_page_compact_workspace_size(int64_t n_pages);
+lsa_status lsa_page_compact(const lsa_page_table *pt, int32_t *table_out, int32_t *refs_out, int32_t *move_src,
+                            int32_t *move_dst, int32_t *n_moves, void *workspace, size_t ws_bytes, void *stream);
+
+/* Copies pages src[i] -> dst[i] of a cache (K, V and their scales) for i < n, or i < min(n, *count) where count
+ * (device int32) is given; src, dst device int32 [n].  Pairs with a negative index or src == dst are skipped; a page
+ * outside [0, n_pages) is skipped and *err = LSA_ERR_INVALID.  No dst may be another pair's src or dst.  One launch. */
+lsa_status lsa_page_copy(const lsa_page_cache *cache, const int32_t *src, const int32_t *dst, int32_t n,
+                         const int32_t *count, int32_t *err, void *stream);
 
 /* ------------------------------------------------------------------------
  * Decode context and lsa_decode_step -- the tau cadence (section 2.1,

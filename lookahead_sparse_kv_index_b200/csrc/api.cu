@@ -62,7 +62,14 @@ extern "C" {
 int32_t lsa_version(void) { return 100; }
 
 int64_t lsa_struct_size(int32_t which) {
-    return which == 0 ? int64_t(sizeof(lsa_params)) : which == 1 ? int64_t(sizeof(lsa_ctx_view)) : -1;
+    switch (which) {
+    case 0: return int64_t(sizeof(lsa_params));
+    case 1: return int64_t(sizeof(lsa_ctx_view));
+    case 10: return int64_t(sizeof(lsa_page_cache));
+    case 11: return int64_t(sizeof(lsa_rope));
+    case 12: return int64_t(sizeof(lsa_page_table));
+    }
+    return -1;
 }
 
 const char *lsa_last_error(void) { return lsa::g_msg; }

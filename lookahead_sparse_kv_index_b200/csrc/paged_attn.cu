@@ -1,0 +1,472 @@
+// Attention of one new token per sequence over a paged key-value cache (lsa_paged_attn):
+//     a_t = scale q . K_t,   out = sum_t softmax(a)_t V_t,   lse = log sum_t exp(a_t).
+//
+// This file holds the entry point, the CUDA-core kernel and the combine.  paged_attn.cuh says how the work is cut.
+//
+// The CUDA-core kernel (fp32 products): a CTA of 8 warps stages `tile` entries of K and V at a time in shared memory
+// through a ring of cp.async stages.  Eight lanes share an entry (each D / 8 of its elements, 16-byte pieces), so a
+// warp holds four entries; every group of eight lanes runs its own online softmax over its entries (max m, sum l and
+// o in registers) for NH query heads, the warps split first the heads and then the entries, and the parts meet once,
+// at the end of a piece.
+#include "paged_attn.cuh"
+
+namespace lsa {
+namespace paged {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kRing = 8;             // tiles whose row offsets are kept: more than any stage count + 1
+constexpr int kMaxTile = 32;
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) { return uint32_t(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool valid) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_wait(int left) {
+    if (left <= 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else if (left == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 2;" ::: "memory");
+}
+
+// Four consecutive elements of a staged row, in fp32.
+template <typename T>
+__device__ __forceinline__ float4 load4(const uint8_t *row, int chunk);
+template <>
+__device__ __forceinline__ float4 load4<float>(const uint8_t *row, int chunk) {
+    return *reinterpret_cast<const float4 *>(row + chunk * 16);
+}
+template <>
+__device__ __forceinline__ float4 load4<uint16_t>(const uint8_t *row, int chunk) {
+    const uint2 u = *reinterpret_cast<const uint2 *>(row + chunk * 8);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ float4 load4<uint8_t>(const uint8_t *row, int chunk) {
+    const uint32_t u = *reinterpret_cast<const uint32_t *>(row + chunk * 4);
+    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(u & 0xffffu), __NV_E4M3);
+    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(u >> 16), __NV_E4M3);
+    const float2 a = __half22float2(__half2(lo)), b = __half22float2(__half2(hi));
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// KC: 4-element chunks of a lane (D <= 32 KC); NH: query heads of a warp.
+template <typename T, int KC, int NH>
+__global__ void __launch_bounds__(kThreads) paged_attn_cc(AttnArgs a, int stages, int nhg) {
+    constexpr bool kScaled = sizeof(T) == 1;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int64_t scratch[40];
+    __shared__ Entry ring[kRing][kMaxTile];
+    const int D = a.cache.D, HS = a.HS, tile = a.tile;
+    const bool latent = a.cache.v == a.cache.k;
+    const int row_bytes = D * int(sizeof(T)), nch = row_bytes / 16;
+    const int stage_bytes = tile * row_bytes * (latent ? 1 : 2) + (kScaled ? tile * 8 : 0);
+    float *qs = reinterpret_cast<float *>(smem + size_t(stages) * stage_bytes);   // [HS][D]
+    float *po = qs + HS * D;                                                      // [TS][HS][D]
+    const int TS = kWarps / nhg;
+    float *pml = po + TS * HS * D;                                                // [TS][HS][2]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = lane >> 3, dl = lane & 7;
+    const int hw = (warp % nhg) * NH, ts = warp / nhg;
+    const float scale2 = a.scale * kLog2e;
+
+    pdl_launch_dependents();
+    pdl_wait();
+    for_pieces<kThreads>(a, scratch, [&](int b, int hseg, int lo, int hi, int slot) {
+        const int kvh = hseg / a.HG, first = (hseg % a.HG) * HS;
+        const int32_t *row = a.table + int64_t(b) * a.table_stride;
+        const int ntiles = (hi - lo + tile - 1) / tile;
+        const uint8_t *kbase = a.cache.k + kvh * a.cache.head_stride, *vbase = a.cache.v + kvh * a.cache.head_stride;
+
+        auto locate = [&](int j) {   // row offsets of tile j
+            if (threadIdx.x < tile && j < ntiles) {
+                const int t = lo + j * tile + threadIdx.x;
+                ring[j % kRing][threadIdx.x] = t < hi ? entry_at(a, row, t) : Entry{-1, 0};
+            }
+        };
+        auto issue = [&](int j) {
+            if (j < ntiles) {
+                const uint32_t st = smem_addr(smem) + uint32_t(j % stages) * stage_bytes;
+                for (int i = threadIdx.x; i < tile * nch; i += kThreads) {
+                    const int r = i / nch, c = i - r * nch;
+                    const Entry e = ring[j % kRing][r];
+                    const bool ok = e.off >= 0;
+                    cp_async16(st + r * row_bytes + c * 16, kbase + (ok ? e.off : 0) + c * 16, ok);
+                    if (!latent)
+                        cp_async16(st + (tile + r) * row_bytes + c * 16, vbase + (ok ? e.off : 0) + c * 16, ok);
+                }
+                if (kScaled && threadIdx.x < tile) {
+                    const Entry e = ring[j % kRing][threadIdx.x];
+                    const bool ok = e.off >= 0;
+                    const int64_t at = ok ? e.slot * a.cache.Hkv + kvh : 0;
+                    const uint32_t sc = st + tile * row_bytes * (latent ? 1 : 2) + threadIdx.x * 4;
+                    cp_async4(sc, a.cache.ks + at, ok);
+                    cp_async4(sc + tile * 4, a.cache.vs + at, ok);
+                }
+            }
+            cp_commit();
+        };
+
+        for (int i = threadIdx.x; i < HS * D; i += kThreads) {
+            const int h = i / D, d = i - h * D;
+            float v = 0.f;
+            if (first + h < a.G) {
+                const int64_t at = (int64_t(kvh) * a.G + first + h) * D + d;
+                const uint8_t *q = static_cast<const uint8_t *>(a.q) + int64_t(b) * a.q_stride;
+                v = a.q_f32 ? reinterpret_cast<const float *>(q)[at]
+                            : bf16_to_f32(reinterpret_cast<const uint16_t *>(q)[at]);
+            }
+            qs[i] = v;
+        }
+        for (int j = 0; j < stages; ++j) locate(j);
+        __syncthreads();
+        for (int j = 0; j < stages - 1; ++j) issue(j);
+
+        float m[NH], l[NH], o[NH][KC * 4];
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+            m[h] = -INFINITY;
+            l[h] = 0.f;
+#pragma unroll
+            for (int e = 0; e < KC * 4; ++e) o[h][e] = 0.f;
+        }
+        for (int i = 0; i < ntiles; ++i) {
+            cp_wait(stages - 2);
+            __syncthreads();
+            issue(i + stages - 1);
+            locate(i + stages);
+            const uint8_t *st = smem + size_t(i % stages) * stage_bytes;
+            const uint8_t *sv = latent ? st : st + tile * row_bytes;
+            const float *sc = reinterpret_cast<const float *>(st + tile * row_bytes * (latent ? 1 : 2));
+            for (int t0 = ts * 4; t0 < tile; t0 += TS * 4) {
+                const int t = min(t0 + grp, tile - 1);
+                const bool ok = t0 + grp < tile && ring[i % kRing][t].off >= 0;
+                const float ks = kScaled ? sc[t] : 1.f, vs = kScaled ? sc[tile + t] : 1.f;
+                float dot[NH];
+#pragma unroll
+                for (int h = 0; h < NH; ++h) dot[h] = 0.f;
+#pragma unroll
+                for (int c = 0; c < KC; ++c) {
+                    const int ch = c * 8 + dl;
+                    if (ch * 4 < D) {
+                        const float4 kx = load4<T>(st + t * row_bytes, ch);
+#pragma unroll
+                        for (int h = 0; h < NH; ++h) {
+                            const float4 q = *reinterpret_cast<const float4 *>(qs + (hw + h) * D + ch * 4);
+                            dot[h] = fmaf(q.x, kx.x, fmaf(q.y, kx.y, fmaf(q.z, kx.z, fmaf(q.w, kx.w, dot[h]))));
+                        }
+                    }
+                }
+                float4 vx[KC];
+#pragma unroll
+                for (int c = 0; c < KC; ++c) {
+                    const int ch = c * 8 + dl;
+                    vx[c] = ch * 4 < D ? load4<T>(sv + t * row_bytes, ch) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {
+                    float s = dot[h];
+#pragma unroll
+                    for (int x = 1; x < 8; x <<= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+                    s = ok ? s * (ks * scale2) : -INFINITY;
+                    const float mn = fmaxf(m[h], s), ref = mn == -INFINITY ? 0.f : mn;
+                    const float f = exp2_approx(m[h] - ref);
+                    const float p = ok ? exp2_approx(s - ref) : 0.f;
+                    m[h] = mn;
+                    l[h] = fmaf(l[h], f, p);
+                    const float pv = p * vs;
+#pragma unroll
+                    for (int c = 0; c < KC; ++c) {
+                        o[h][c * 4] = fmaf(pv, vx[c].x, o[h][c * 4] * f);
+                        o[h][c * 4 + 1] = fmaf(pv, vx[c].y, o[h][c * 4 + 1] * f);
+                        o[h][c * 4 + 2] = fmaf(pv, vx[c].z, o[h][c * 4 + 2] * f);
+                        o[h][c * 4 + 3] = fmaf(pv, vx[c].w, o[h][c * 4 + 3] * f);
+                    }
+                }
+            }
+        }
+        cp_wait(0);
+        // join the warp's four groups, then leave the warp's part in shared memory
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+            float M = m[h];
+            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
+            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
+            const float f = exp2_approx(m[h] - (M == -INFINITY ? 0.f : M));
+            float L = l[h] * f;
+            L += __shfl_xor_sync(0xffffffffu, L, 8);
+            L += __shfl_xor_sync(0xffffffffu, L, 16);
+#pragma unroll
+            for (int e = 0; e < KC * 4; ++e) {
+                float v = o[h][e] * f;
+                v += __shfl_xor_sync(0xffffffffu, v, 8);
+                v += __shfl_xor_sync(0xffffffffu, v, 16);
+                const int d = ((e >> 2) * 8 + dl) * 4 + (e & 3);
+                if (grp == 0 && d < D) po[(ts * HS + hw + h) * D + d] = v;
+            }
+            if (lane == 0) {
+                pml[(ts * HS + hw + h) * 2] = M;
+                pml[(ts * HS + hw + h) * 2 + 1] = L;
+            }
+        }
+        __syncthreads();
+        finish_piece(a, b, hseg, slot, TS, po, pml);
+        __syncthreads();
+    });
+    if (blockIdx.x == 0 && a.err)
+        for (int b = threadIdx.x; b < a.B; b += kThreads)
+            if (a.seq_len[b] > a.reach) raise_err(a.err, LSA_ERR_CAPACITY);
+}
+
+// Joins a segment's partials (paged_attn.cuh).  CTA (c, i), c >= 1, acts where the segment that its unit c * share cuts
+// was begun by CTA c - 1, for head i of the group; CTA (c, i) also writes sequences c, c + grid, ... that are empty.
+constexpr int kCombineThreads = 128;
+__global__ void __launch_bounds__(kCombineThreads) paged_attn_combine(AttnArgs a, int grid) {
+    __shared__ int64_t scratch[40];
+    __shared__ float red[8];
+    extern __shared__ float wgt[];   // [grid]
+    const int c = blockIdx.x, h = blockIdx.y, D = a.cache.D, HS = a.HS;
+    pdl_launch_dependents();
+    pdl_wait();
+    for (int b = c; b < a.B; b += grid) {
+        if (tiles_of(a, b) != 0) continue;
+        for (int g = 0; g < a.cache.Hkv * a.HG; ++g) {
+            const int in = (g % a.HG) * HS + h;
+            if (in >= a.G) continue;
+            const int64_t hq = int64_t(b) * a.Hq + (g / a.HG) * a.G + in;
+            for (int d = threadIdx.x; d < D; d += kCombineThreads) store_out(a, hq * D + d, 0.f);
+            if (threadIdx.x == 0 && a.lse) a.lse[hq] = -INFINITY;
+        }
+    }
+    const Where w = find_start<kCombineThreads>(a, c, grid, scratch);
+    if (w.b < 0) return;
+    const int64_t n = tiles_of(a, w.b), u = int64_t(c) * w.share;
+    const int hseg = int((u - w.base) / n);
+    const int64_t s0 = w.base + hseg * n;
+    const int64_t c0 = s0 / w.share, c1 = (s0 + n - 1) / w.share;
+    if (u == s0 || c != c0 + 1) return;
+    const int in = (hseg % a.HG) * HS + h;
+    if (in >= a.G) return;
+    const int P = int(c1 - c0) + 1;
+    auto slot = [&](int p) { return p == 0 ? 2 * c0 + 1 : 2 * (c0 + p); };
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float M = -INFINITY;
+    for (int p = threadIdx.x; p < P; p += kCombineThreads) M = fmaxf(M, a.part_ml[(slot(p) * HS + h) * 2]);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    if (lane == 0) red[warp] = M;
+    __syncthreads();
+    M = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    const float ref = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    for (int p = threadIdx.x; p < P; p += kCombineThreads) {
+        const float f = exp2f(a.part_ml[(slot(p) * HS + h) * 2] - ref);
+        wgt[p] = f;
+        L = fmaf(f, a.part_ml[(slot(p) * HS + h) * 2 + 1], L);
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
+    if (lane == 0) red[4 + warp] = L;
+    __syncthreads();
+    L = (red[4] + red[5]) + (red[6] + red[7]);
+    const int64_t hq = int64_t(w.b) * a.Hq + (hseg / a.HG) * a.G + in;
+    for (int d = threadIdx.x; d < D; d += kCombineThreads) {
+        float v = 0.f;
+#pragma unroll 8
+        for (int p = 0; p < P; ++p) v = fmaf(wgt[p], a.part_o[(slot(p) * HS + h) * D + d], v);
+        store_out(a, hq * D + d, L == 0.f ? 0.f : v / L);
+    }
+    if (threadIdx.x == 0 && a.lse) a.lse[hq] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+int ceil_pow2(int x) {
+    int p = 1;
+    while (p < x) p *= 2;
+    return p;
+}
+
+// KC of a head dim, and the heads of a warp that keep o within 64 registers.
+int cc_chunks(int D) {
+    const int need = (D + 31) / 32;
+    for (int k : {1, 2, 3, 4, 6, 8})
+        if (need <= k) return k;
+    return 16;
+}
+int cc_heads(int kc) { return kc <= 2 ? 8 : kc <= 4 ? 4 : kc <= 8 ? 2 : 1; }
+
+AttnPlan plan_cc(const lsa_page_cache &c, int Hq) {
+    AttnPlan p = {};
+    const int G = Hq / c.Hkv, nh = cc_heads(cc_chunks(c.D));
+    const int nhg = ceil_pow2(G >= kWarps * nh ? kWarps : (G + nh - 1) / nh);
+    p.HS = nhg * nh;
+    p.HG = (G + p.HS - 1) / p.HS;
+    const size_t entry = size_t(c.D) * elem_size(c.dtype) * (c.v == c.k ? 1 : 2) + (c.dtype == LSA_E4M3 ? 8 : 0);
+    p.tile = kMaxTile;
+    while (p.tile > 4 && p.tile * entry > 24 * 1024) p.tile /= 2;
+    p.stages = 4;
+    p.threads = kThreads;
+    p.smem = p.stages * p.tile * entry + (size_t(p.HS) * c.D + size_t(kWarps / nhg) * p.HS * (c.D + 2)) * 4;
+    p.grid = sm_count() * 2;
+    p.ok = true;
+    return p;
+}
+
+template <typename T, int KC, int NH>
+lsa_status launch_cc(const AttnArgs &a, const AttnPlan &p, int grid, cudaStream_t st) {
+    LSA_CUDA(ensure_smem(paged_attn_cc<T, KC, NH>, p.smem));
+    LSA_CUDA(launch_pdl(paged_attn_cc<T, KC, NH>, dim3(grid), dim3(kThreads), p.smem, st, a, int(p.stages),
+                        int(p.HS / NH)));
+    LSA_LAUNCHED("paged_attn_cc");
+    return LSA_OK;
+}
+
+template <typename T>
+lsa_status dispatch_cc(const AttnArgs &a, const AttnPlan &p, int grid, cudaStream_t st) {
+    switch (cc_chunks(a.cache.D)) {
+    case 1: return launch_cc<T, 1, 8>(a, p, grid, st);
+    case 2: return launch_cc<T, 2, 8>(a, p, grid, st);
+    case 3: return launch_cc<T, 3, 4>(a, p, grid, st);
+    case 4: return launch_cc<T, 4, 4>(a, p, grid, st);
+    case 6: return launch_cc<T, 6, 2>(a, p, grid, st);
+    case 8: return launch_cc<T, 8, 2>(a, p, grid, st);
+    default: return launch_cc<T, 16, 1>(a, p, grid, st);
+    }
+}
+
+AttnPlan plan_of(const lsa_page_cache &c, int Hq) { return plan_cc(c, Hq); }
+
+// A segment of so few units is done by one CTA, without partials and a second launch.
+constexpr int kWholeUnits = 8;
+
+}  // namespace
+
+lsa_status check_cache(const lsa_page_cache *c, const char *who) {
+    LSA_CHECK_ARG(c, "%s: a cache is required", who);
+    LSA_CHECK_ARG(c->k && c->v, "%s: the cache's k and v are required", who);
+    LSA_CHECK_ARG(valid_dtype(c->dtype), "%s: unknown cache dtype", who);
+    LSA_CHECK_ARG(c->page_size >= 1 && c->Hkv >= 1 && c->D >= 1 && c->n_pages >= 1,
+                  "%s: the cache's page_size=%d Hkv=%d D=%d n_pages=%lld must be positive", who, c->page_size, c->Hkv,
+                  c->D, (long long)c->n_pages);
+    LSA_CHECK_SUPPORTED(c->D % 16 == 0 && c->D <= 512, "%s: D=%d is not a multiple of 16 up to 512", who, c->D);
+    LSA_CHECK_SUPPORTED(c->Hkv <= 65535, "%s: Hkv=%d > 65535", who, c->Hkv);
+    LSA_CHECK_ARG(c->n_pages < (int64_t(1) << 31) && c->n_pages * c->page_size < (int64_t(1) << 31),
+                  "%s: the cache has 2^31 entries or more", who);
+    const bool scaled = c->dtype == LSA_E4M3;
+    LSA_CHECK_ARG(scaled == (c->k_scale != nullptr) && scaled == (c->v_scale != nullptr),
+                  "%s: k_scale and v_scale are required for E4M3 rows and only for them", who);
+    LSA_CHECK_ARG(c->v != c->k || c->v_scale == c->k_scale, "%s: a latent cache (v == k) has v_scale == k_scale", who);
+    const int64_t e = int64_t(elem_size(c->dtype)), lim = int64_t(1) << 56;
+    const struct {
+        int64_t stride, extent;
+        const char *name;
+    } dims[3] = {{c->page_stride, c->n_pages, "page_stride"}, {c->slot_stride, c->page_size, "slot_stride"},
+                 {c->head_stride, c->Hkv, "head_stride"}};
+    for (const auto &d : dims) {
+        LSA_CHECK_ARG(d.stride >= (d.extent > 1 ? c->D : 0) && d.stride < lim / (e * d.extent),
+                      "%s: %s=%lld", who, d.name, (long long)d.stride);
+        LSA_CHECK_ARG(d.stride * e % 16 == 0, "%s: %s=%lld elements is not a multiple of 16 bytes", who, d.name,
+                      (long long)d.stride);
+    }
+    LSA_CHECK_ARG(aligned16(c->k) && aligned16(c->v), "%s: k and v must be 16-byte aligned", who);
+    return LSA_OK;
+}
+
+lsa_status paged_combine(const AttnArgs &a, int grid, cudaStream_t st) {
+    const int heads = a.HS < a.G ? a.HS : a.G;
+    LSA_CUDA(launch_pdl(paged_attn_combine, dim3(grid, heads), dim3(kCombineThreads), size_t(grid) * 4, st, a, grid));
+    LSA_LAUNCHED("paged_attn_combine");
+    return LSA_OK;
+}
+
+}  // namespace paged
+}  // namespace lsa
+
+using namespace lsa;
+using namespace lsa::paged;
+
+static size_t workspace_bytes(const AttnPlan &p, int D) { return size_t(p.grid) * 2 * p.HS * (D + 2) * 4; }
+
+static lsa_status check_heads(const lsa_page_cache *cache, int32_t Hq, const char *who) {
+    LSA_CHECK_ARG(Hq >= 1 && Hq % cache->Hkv == 0, "%s: Hq=%d is not a positive multiple of Hkv=%d", who, Hq,
+                  cache->Hkv);
+    LSA_CHECK_SUPPORTED(Hq <= 65535, "%s: Hq=%d > 65535", who, Hq);
+    return LSA_OK;
+}
+
+extern "C" size_t lsa_paged_attn_workspace_size(const lsa_page_cache *cache, int32_t B, int32_t Hq) {
+    clear_error();
+    if (check_cache(cache, "lsa_paged_attn_workspace_size") != LSA_OK || B < 1 ||
+        check_heads(cache, Hq, "lsa_paged_attn_workspace_size") != LSA_OK)
+        return 0;
+    return workspace_bytes(plan_of(*cache, Hq), cache->D);
+}
+
+extern "C" lsa_status lsa_paged_attn(const void *Q, lsa_dtype q_dtype, int64_t q_stride, const lsa_page_cache *cache,
+                                     const int32_t *table, int64_t table_stride, int32_t max_pages,
+                                     const int32_t *seq_len, int32_t B, int32_t Hq, int32_t window, float scale,
+                                     void *out, float *lse, void *workspace, size_t ws_bytes, int32_t *err,
+                                     void *stream) {
+    clear_error();
+    LSA_CHECK_ARG(Q && table && seq_len && out && workspace,
+                  "lsa_paged_attn: Q, table, seq_len, out and workspace are required");
+    lsa_status s = check_cache(cache, "lsa_paged_attn");
+    if (s != LSA_OK) return s;
+    LSA_CHECK_ARG(B >= 1, "lsa_paged_attn: B=%d", B);
+    s = check_heads(cache, Hq, "lsa_paged_attn");
+    if (s != LSA_OK) return s;
+    LSA_CHECK_ARG(valid_dtype(q_dtype), "lsa_paged_attn: unknown q_dtype");
+    LSA_CHECK_SUPPORTED(q_dtype == (cache->dtype == LSA_F32 ? LSA_F32 : LSA_BF16),
+                        "lsa_paged_attn: Q must be F32 with an F32 cache and BF16 with a BF16 or E4M3 one");
+    const int64_t e = int64_t(elem_size(q_dtype));
+    LSA_CHECK_ARG(q_stride >= int64_t(Hq) * cache->D && q_stride < (int64_t(1) << 40) && q_stride * e % 16 == 0,
+                  "lsa_paged_attn: q_stride=%lld is less than Hq * D or no multiple of 16 bytes", (long long)q_stride);
+    LSA_CHECK_ARG(aligned16(Q) && aligned16(out), "lsa_paged_attn: Q and out must be 16-byte aligned");
+    LSA_CHECK_ARG(max_pages >= 1 && table_stride >= max_pages && table_stride < (int64_t(1) << 40),
+                  "lsa_paged_attn: max_pages=%d table_stride=%lld", max_pages, (long long)table_stride);
+    LSA_CHECK_ARG(int64_t(max_pages) * cache->page_size < (int64_t(1) << 31),
+                  "lsa_paged_attn: a table row reaches 2^31 entries or more");
+    LSA_CHECK_ARG(window >= 0, "lsa_paged_attn: window=%d", window);
+    LSA_CHECK_ARG(scale > 0.0f && scale < 1e30f, "lsa_paged_attn: scale must be positive and finite");
+    const AttnPlan p = plan_of(*cache, Hq);
+    LSA_CHECK_ARG(ws_bytes >= workspace_bytes(p, cache->D) && aligned16(workspace),
+                  "lsa_paged_attn: workspace of %zu bytes < %zu", ws_bytes, workspace_bytes(p, cache->D));
+
+    AttnArgs a = {};
+    a.cache = view_of(*cache);
+    a.q = Q;
+    a.q_stride = q_stride * e;
+    a.table = table;
+    a.table_stride = table_stride;
+    a.reach = int64_t(max_pages) * cache->page_size;
+    a.seq_len = seq_len;
+    a.B = B;
+    a.Hq = Hq;
+    a.G = Hq / cache->Hkv;
+    a.HG = p.HG;
+    a.HS = p.HS;
+    a.window = window;
+    a.scale = scale;
+    a.out = out;
+    a.lse = lse;
+    a.part_o = static_cast<float *>(workspace);
+    a.part_ml = a.part_o + int64_t(p.grid) * 2 * p.HS * cache->D;
+    a.err = err;
+    a.tile = p.tile;
+    a.min_share = 1;
+    a.q_f32 = q_dtype == LSA_F32;
+    const int64_t most = window > 0 && window < a.reach ? window : a.reach;
+    const int64_t segments = int64_t(B) * cache->Hkv * p.HG;
+    a.whole = most <= int64_t(kWholeUnits) * p.tile && segments < (int64_t(1) << 31);
+    const int grid = a.whole ? int(segments) : p.grid;
+    cudaStream_t st = as_stream(stream);
+    if (cache->dtype == LSA_F32) s = dispatch_cc<float>(a, p, grid, st);
+    else if (cache->dtype == LSA_BF16) s = dispatch_cc<uint16_t>(a, p, grid, st);
+    else s = dispatch_cc<uint8_t>(a, p, grid, st);
+    if (s != LSA_OK || a.whole) return s;
+    return paged_combine(a, grid, st);
+}

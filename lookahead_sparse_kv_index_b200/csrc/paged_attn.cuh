@@ -1,0 +1,213 @@
+// Attention of one new token over a paged cache: what its two kernels and the combine share.
+//
+// The work is cut into units of `tile` entries of one segment: a segment is one sequence's one group of up to `HS`
+// query heads of a kv head.  Units are numbered sequence by sequence, head group by head group, and CTA c of the
+// grid owns the `share` consecutive units from c * share on, so every SM reads the same number of entries whatever
+// the sequences' lengths are.  A segment that lies in one CTA's share is finished there; of the others each CTA
+// writes a partial (unnormalised o, and the running max m and sum l of its softmax, both for 2^x), and the combine
+// kernel joins a segment's partials in unit order:
+//     M = max m_c,  L = sum l_c 2^(m_c - M),  o = sum o_c 2^(m_c - M) / L,  lse = (M + log2 L) ln 2.
+// A CTA has at most two partials: slot 2c for the piece that continues a segment, 2c + 1 for one that begins it.
+#pragma once
+
+#include "paged.cuh"
+
+namespace lsa {
+namespace paged {
+
+struct AttnArgs {
+    CacheView cache;
+    const void *q;
+    int64_t q_stride;            // bytes
+    const int32_t *table;
+    int64_t table_stride;
+    int64_t reach;               // max_pages * page_size
+    const int32_t *seq_len;
+    int32_t B, Hq, G;            // G = Hq / Hkv query heads of a kv head
+    int32_t HG, HS;              // head groups of a kv head, query heads of a group
+    int32_t window;
+    float scale;
+    void *out;
+    float *lse;
+    float *part_o, *part_ml;     // [2 * grid][HS][D], [2 * grid][HS][2]
+    int32_t *err;
+    int32_t tile, min_share;
+    int32_t whole;               // 1: CTA c does segment c and no partials are written
+    int32_t q_f32;
+};
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Entries [lo, hi) of sequence b that are attended.
+struct Seen {
+    int32_t lo, hi;
+};
+__device__ __forceinline__ Seen seen_of(const AttnArgs &a, int b) {
+    int64_t n = a.seq_len[b];
+    n = n < 0 ? 0 : n > a.reach ? a.reach : n;
+    Seen s;
+    s.hi = int32_t(n);
+    s.lo = a.window > 0 && n > a.window ? int32_t(n - a.window) : 0;
+    return s;
+}
+__device__ __forceinline__ int32_t tiles_of(const AttnArgs &a, int b) {
+    const Seen s = seen_of(a, b);
+    return (s.hi - s.lo + a.tile - 1) / a.tile;
+}
+
+// Where a unit lies: sequence b, whose first unit is `base`.
+struct Where {
+    int64_t total, share;   // units of the call, units of a CTA
+    int64_t base;
+    int32_t b;              // -1: past the last unit
+};
+
+// Finds the owner of unit `grid index * share` (whole block; `scratch`: 40 int64 of shared memory).
+template <int THREADS>
+__device__ Where find_start(const AttnArgs &a, int64_t cta, int64_t grid, int64_t *scratch) {
+    constexpr int kWarps = THREADS / 32;
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const int per = (a.B + THREADS - 1) / THREADS;
+    const int b0 = min(a.B, t * per), b1 = min(a.B, b0 + per);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) mine += tiles_of(a, b);
+    int64_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += up;
+    }
+    if (lane == 31) scratch[warp] = inc;
+    if (t == 0) scratch[34] = -1;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += scratch[w];
+        total += scratch[w];
+    }
+    const int64_t heads = int64_t(a.cache.Hkv) * a.HG;
+    Where r;
+    r.total = total * heads;
+    r.share = (r.total + grid - 1) / grid;
+    if (r.share < a.min_share) r.share = a.min_share;
+    const int64_t start = cta * r.share;
+    int64_t pre = before + inc - mine;
+    if (start >= pre * heads && start < (pre + mine) * heads) {
+        for (int b = b0; b < b1; ++b) {
+            const int64_t n = tiles_of(a, b);
+            if (start < (pre + n) * heads) {
+                scratch[34] = b;
+                scratch[35] = pre * heads;
+                break;
+            }
+            pre += n;
+        }
+    }
+    __syncthreads();
+    r.b = int32_t(scratch[34]);
+    r.base = scratch[35];
+    __syncthreads();
+    return r;
+}
+
+// Where entry t of a sequence (its table row `row`) lies: the byte offset of its rows in K and V (head 0), negative
+// where the table names no page of the pool, and the flat index of its slot (page * page_size + slot).
+struct Entry {
+    int64_t off, slot;
+};
+__device__ __forceinline__ Entry entry_at(const AttnArgs &a, const int32_t *row, int t) {
+    const int p = t / a.cache.page_size, s = t - p * a.cache.page_size;
+    const int64_t page = row[p];
+    if (page < 0 || page >= a.cache.n_pages) {
+        raise_err(a.err, LSA_ERR_INVALID);
+        return Entry{-1, 0};
+    }
+    return Entry{page * a.cache.page_stride + s * a.cache.slot_stride, page * a.cache.page_size + s};
+}
+
+// The pieces of a CTA, in unit order: f(b, hseg, lo, hi, slot) for entries [lo, hi) of sequence b and segment hseg (kv
+// head hseg / HG, head group hseg % HG); slot: where the piece's partial goes, -1 where the piece is a whole segment.
+template <int THREADS, typename F>
+__device__ __forceinline__ void for_pieces(const AttnArgs &a, int64_t *scratch, F f) {
+    const int heads = a.cache.Hkv * a.HG;
+    if (a.whole) {
+        const int b = blockIdx.x / heads;
+        const Seen s = seen_of(a, b);
+        f(b, int(blockIdx.x) - b * heads, s.lo, s.hi, -1);
+        return;
+    }
+    const Where w = find_start<THREADS>(a, blockIdx.x, gridDim.x, scratch);
+    if (w.b < 0) return;
+    int b = w.b;
+    int64_t base = w.base, u = int64_t(blockIdx.x) * w.share;
+    const int64_t end = u + w.share < w.total ? u + w.share : w.total;
+    while (u < end) {
+        const Seen s = seen_of(a, b);
+        const int n = (s.hi - s.lo + a.tile - 1) / a.tile;
+        if (u - base >= int64_t(n) * heads) {   // past this sequence
+            base += int64_t(n) * heads;
+            ++b;
+            continue;
+        }
+        const int hseg = int((u - base) / n), t0 = int((u - base) - int64_t(hseg) * n);
+        const int t1 = int(end - u < n - t0 ? t0 + (end - u) : n);
+        const int lo = s.lo + t0 * a.tile, hi = t1 == n ? s.hi : s.lo + t1 * a.tile;
+        f(b, hseg, lo, hi, t0 == 0 && t1 == n ? -1 : 2 * int(blockIdx.x) + (t0 == 0));
+        u += t1 - t0;
+    }
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void store_out(const AttnArgs &a, int64_t i, float v) {
+    if (a.q_f32) static_cast<float *>(a.out)[i] = v;
+    else static_cast<__nv_bfloat16 *>(a.out)[i] = __float2bfloat16_rn(v);
+}
+
+// Ends a piece (whole block): joins the `n` parts that its warps left in shared memory, o [n][HS][D], ml [n][HS][2],
+// and writes the segment's output or the piece's partial.
+__device__ __forceinline__ void finish_piece(const AttnArgs &a, int b, int hseg, int slot, int n, const float *o,
+                                             const float *ml) {
+    const int D = a.cache.D, HS = a.HS;
+    const int first = (hseg % a.HG) * HS, heads = min(HS, a.G - first);
+    const int64_t hq = int64_t(b) * a.Hq + (hseg / a.HG) * a.G + first;
+    for (int i = threadIdx.x; i < heads * D; i += blockDim.x) {
+        const int h = i / D, d = i - h * D;
+        float M = -INFINITY;
+        for (int p = 0; p < n; ++p) M = fmaxf(M, ml[(p * HS + h) * 2]);
+        const float ref = M == -INFINITY ? 0.f : M;
+        float L = 0.f, v = 0.f;
+        for (int p = 0; p < n; ++p) {
+            const float w = exp2f(ml[(p * HS + h) * 2] - ref);
+            L += w * ml[(p * HS + h) * 2 + 1];
+            v += w * o[(int64_t(p) * HS + h) * D + d];
+        }
+        if (slot < 0) {
+            store_out(a, (hq + h) * D + d, L == 0.f ? 0.f : v / L);
+            if (d == 0 && a.lse) a.lse[hq + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+        } else {
+            a.part_o[(int64_t(slot) * HS + h) * D + d] = v;
+            if (d == 0) {
+                a.part_ml[(int64_t(slot) * HS + h) * 2] = M;
+                a.part_ml[(int64_t(slot) * HS + h) * 2 + 1] = L;
+            }
+        }
+    }
+}
+
+// Host side.  How a call is cut: query heads of a group, units, CTAs (a function of the cache's shape and the device
+// alone, so that the workspace's size does not depend on the call's lengths).
+struct AttnPlan {
+    int32_t HG, HS, tile, grid, threads, stages;
+    size_t smem;
+    bool ok;
+};
+lsa_status paged_combine(const AttnArgs &a, int grid, cudaStream_t st);
+
+}  // namespace paged
+}  // namespace lsa

@@ -38,7 +38,9 @@ EXPORTS = [
     "lsa_ctx_set_graphs", "lsa_ctx_set_timing", "lsa_ctx_stage_times", "lsa_ctx_reset_counters",
     "lsa_ctx_launches", "lsa_selftest_bounded_wait", "lsa_index_union", "lsa_query_encode",
     "lsa_attn_set_merge", "lsa_struct_size", "lsa_ctx_flush_cache", "lsa_index_score_select_workspace_size",
-    "lsa_index_score_select",
+    "lsa_index_score_select", "lsa_paged_attn_workspace_size", "lsa_paged_attn", "lsa_qk_norm_rope",
+    "lsa_rope_frequencies", "lsa_page_grow", "lsa_page_fork", "lsa_page_free", "lsa_page_compact_workspace_size",
+    "lsa_page_compact", "lsa_page_copy",
 ]
 
 
@@ -64,6 +66,20 @@ class View(ctypes.Structure):
     _fields_ = [("z", P), ("z_kept", P), ("kept_idx", P), ("kept_off", P), ("slot_of", P), ("hot", P),
                 ("topk_idx", P), ("topk_pos", P), ("topk_cnt", P), ("err", P), ("kept_slot", P), ("owner", P),
                 ("fetched", P), ("attn_rows", P), ("attn_row_cap", i64), ("win_base", i64), ("hca_base", i64)]
+
+
+class PageCacheDesc(ctypes.Structure):
+    _fields_ = [("k", P), ("v", P), ("k_scale", P), ("v_scale", P), ("dtype", i32), ("page_size", i32), ("Hkv", i32),
+                ("D", i32), ("n_pages", i64), ("page_stride", i64), ("slot_stride", i64), ("head_stride", i64)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("freq", P), ("rot_dim", i32), ("interleaved", i32), ("inverse", i32), ("mscale", f32)]
+
+
+class PageTableDesc(ctypes.Structure):
+    _fields_ = [("table", P), ("len", P), ("refs", P), ("n_rows", i32), ("max_pages", i32), ("page_size", i32),
+                ("n_pages", i64)]
 
 
 def _sig(name, res, args):
@@ -104,6 +120,18 @@ _sig("lsa_selftest_bounded_wait", i32, [i64, P, P, P])
 _sig("lsa_index_union", i32, [ctypes.POINTER(P), i32, i64, P, P])
 _sig("lsa_query_encode", i32, [P, i32, i32, P, i32, P, i32, i32, P, P, i32, P, P, P])
 _sig("lsa_attn_set_merge", i32, [P, P, P, P, i32, i32, i32, i32, P, i32, P, i32, P, P, P])
+_sig("lsa_paged_attn_workspace_size", sz, [P, i32, i32])
+_sig("lsa_paged_attn", i32, [P, i32, i64, P, P, i64, i32, P, i32, i32, i32, f32, P, P, P, sz, P, P])
+_sig("lsa_qk_norm_rope", i32, [P, i64, P, i64, P, i64, P, i64, P, i64, i32, i64, i32, i32, i32, P, P, f32, P, P, P, P,
+                               i64, i32, i32, P, P, P, P])
+_sig("lsa_rope_frequencies", i32, [i32, i32, ctypes.c_double, ctypes.c_double, i64, ctypes.c_double, ctypes.c_double,
+                                   P, P])
+_sig("lsa_page_grow", i32, [P, P, P, P])
+_sig("lsa_page_fork", i32, [P, P, P, i32, P, P, P, P])
+_sig("lsa_page_free", i32, [P, P, i32, P, P])
+_sig("lsa_page_compact_workspace_size", sz, [i64])
+_sig("lsa_page_compact", i32, [P, P, P, P, P, P, P, sz, P])
+_sig("lsa_page_copy", i32, [P, P, P, i32, P, P, P])
 
 lib = _L
 
@@ -237,6 +265,253 @@ def sparse_attn(Q, dtype, kv, kv_row_stride, k_off, v_off, rows, B, Hq, D, k, sc
                               k, float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
                               workspace.numel() * workspace.element_size(), _ptr(err), _stream(stream)),
            "lsa_sparse_attn")
+
+
+# -------------------------------------------------------------- paged cache
+#
+# These bindings read sizes, strides and types off the tensors, so they check them: a mismatch is a ValueError, and
+# what the library refuses is an LsaError.  They run on the device that holds the tensors, on its current stream
+# unless `stream` is given (a stream of that device).
+
+_ELEM = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3}
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _i32(t, name, device, shape):
+    _need(t.dtype == torch.int32 and t.device == device and t.is_contiguous() and tuple(t.shape) == tuple(shape),
+          f"{name}: a contiguous int32 tensor {list(shape)} on {device} is needed, not {t.dtype} {list(t.shape)} on "
+          f"{t.device}")
+    return t.data_ptr()
+
+
+def _err_word(err, device):
+    _need(err is None or (err.dtype == torch.int32 and err.device == device and err.numel() == 1),
+          "err: one int32 on the call's device is needed")
+    return _ptr(err)
+
+
+def _on(device, f, args, where, stream):
+    """Calls the library with `device` current and its current stream, or the one given, as the last argument."""
+    _need(device.type == "cuda", f"{where}: tensors on a CUDA device are needed, not on {device}")
+    _need(stream is None or stream.device == device, f"{where}: the stream is not one of {device}")
+    if device.index == torch.cuda.current_device():
+        _check(f(*args, (stream or torch.cuda.current_stream()).cuda_stream), where)
+        return
+    with torch.cuda.device(device):
+        _check(f(*args, (stream or torch.cuda.current_stream()).cuda_stream), where)
+
+
+class PageCache:
+    """One layer's paged key-value cache (lsa_page_cache in lsa.h).
+
+    k, v: tensors [n_pages, page_size, Hkv, D] of float32, bfloat16 or float8_e4m3fn with the same strides, unit
+    stride in D (a permuted view of another layout is fine); v None: a latent cache, whose rows are keys and values.
+    k_scale, v_scale: contiguous float32 [n_pages, page_size, Hkv] for float8_e4m3fn rows.
+    """
+
+    def __init__(self, k, v=None, k_scale=None, v_scale=None):
+        _need(k.dim() == 4 and k.dtype in _ELEM and (k.stride(3) == 1 or k.shape[3] == 1),
+              "k: [n_pages, page_size, Hkv, D] of float32, bfloat16 or float8_e4m3fn with unit stride in D is needed")
+        _need(v is None or (v.shape == k.shape and v.stride() == k.stride() and v.dtype == k.dtype
+                            and v.device == k.device), "v: the shape, strides, type and device of k are needed")
+        self.latent = v is None or v.data_ptr() == k.data_ptr()
+        _need(not (v is None and v_scale is not None), "v_scale goes with v")
+        for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+            _need(s is None or (s.dtype == torch.float32 and s.shape == k.shape[:3] and s.is_contiguous()
+                                and s.device == k.device),
+                  f"{name}: a contiguous float32 tensor {list(k.shape[:3])} on {k.device} is needed")
+        if v is None:
+            v, v_scale = k, k_scale
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device = k.device
+        self.n_pages, self.page_size, self.Hkv, self.D = k.shape
+        self.desc = PageCacheDesc(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ELEM[k.dtype], self.page_size,
+                                  self.Hkv, self.D, self.n_pages, k.stride(0), k.stride(1), k.stride(2))
+        self._ref = ctypes.byref(self.desc)
+
+
+def paged_attn_workspace_size(cache, B, Hq) -> int:
+    if cache.device.type != "cuda" or cache.device.index == torch.cuda.current_device():
+        n = _L.lsa_paged_attn_workspace_size(cache._ref, B, Hq)
+    else:
+        with torch.cuda.device(cache.device):
+            n = _L.lsa_paged_attn_workspace_size(cache._ref, B, Hq)
+    _need(n > 0, _L.lsa_last_error().decode() or f"B={B} must be positive")
+    return int(n)
+
+
+def _table_args(table, device):
+    _need(table.dtype == torch.int32 and table.dim() == 2 and table.device == device
+          and (table.stride(1) == 1 or table.shape[1] == 1),
+          f"table: int32 [rows, max_pages] on {device} with unit stride along a row is needed")
+    return table.data_ptr(), max(table.stride(0), table.shape[1]) if table.shape[0] == 1 else table.stride(0)
+
+
+def paged_attn(Q, cache, table, seq_len, out, workspace, lse=None, window=0, scale=None, err=None, stream=None):
+    """Attention of one new token per sequence over a PageCache (lsa_paged_attn).
+
+    Q [B, Hq, D] (any stride between sequences), table int32 [B, max_pages], seq_len int32 [B]; out [B, Hq, D] and
+    lse float32 [B, Hq] contiguous; workspace: a contiguous tensor of paged_attn_workspace_size bytes.  window: attend
+    only the last `window` entries (0: all).  scale None: 1 / sqrt(D).
+    """
+    dev = cache.device
+    _need(Q.dim() == 3 and Q.shape[2] == cache.D and Q.dtype in _ELEM and Q.device == dev
+          and (Q.stride(2) == 1 or Q.shape[2] == 1) and (Q.stride(1) == cache.D or Q.shape[1] == 1),
+          f"Q: [B, Hq, {cache.D}] on {dev} with heads side by side is needed")
+    B, Hq, D = Q.shape
+    _need(out.shape == Q.shape and out.dtype == Q.dtype and out.device == dev and out.is_contiguous(),
+          "out: contiguous, of Q's shape, type and device, is needed")
+    _need(lse is None or (lse.dtype == torch.float32 and tuple(lse.shape) == (B, Hq) and lse.device == dev
+                          and lse.is_contiguous()), "lse: contiguous float32 [B, Hq] is needed")
+    _need(workspace.device == dev and workspace.is_contiguous(), "workspace: a contiguous tensor on the cache's device")
+    _need(table.dim() == 2 and table.shape[0] == B, f"table: {B} rows are needed")
+    tp, ts = _table_args(table, dev)
+    _on(dev, _L.lsa_paged_attn,
+        (Q.data_ptr(), _ELEM[Q.dtype], Q.stride(0) if B > 1 else Hq * D, cache._ref, tp, ts, table.shape[1],
+         _i32(seq_len, "seq_len", dev, (B,)), B, Hq, int(window), float(D ** -0.5 if scale is None else scale),
+         out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+         _err_word(err, dev)), "lsa_paged_attn", stream)
+
+
+ROPE_KINDS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def rope_frequencies(rot_dim, base=10000.0, kind="plain", factor=1.0, orig_len=0, beta_fast=32.0, beta_slow=1.0):
+    """(frequencies float64 [rot_dim / 2] on the host, mscale) of a plain or scaled rotation (lsa_rope_frequencies)."""
+    _need(kind in ROPE_KINDS, f"kind: one of {', '.join(ROPE_KINDS)} is needed, not {kind!r}")
+    freq, m = torch.empty(max(0, rot_dim // 2), dtype=torch.float64), ctypes.c_float()
+    _check(_L.lsa_rope_frequencies(ROPE_KINDS[kind], rot_dim, base, factor, orig_len, beta_fast, beta_slow,
+                                   freq.data_ptr(), ctypes.byref(m)), "lsa_rope_frequencies")
+    return freq, float(m.value)
+
+
+class Rope:
+    """A rotation by position (lsa_rope in lsa.h).  freq: contiguous float64 [rot_dim / 2] on the device, radians per
+    position (rope_frequencies gives plain and scaled ones)."""
+
+    def __init__(self, freq, interleaved=False, inverse=False, mscale=1.0):
+        _need(freq.dtype == torch.float64 and freq.dim() == 1 and freq.is_contiguous(),
+              "freq: a contiguous float64 vector is needed")
+        _need(mscale > 0, "mscale must be positive")
+        self.freq = freq
+        self.desc = RopeDesc(_ptr(freq), 2 * freq.numel(), int(interleaved), int(inverse), mscale)
+        self._ref = ctypes.byref(self.desc)
+
+
+def _heads(t, name, T, H, D, dtype, device):
+    _need(t.dim() == 3 and tuple(t.shape) == (T, H, D) and t.dtype == dtype and t.device == device
+          and (t.stride(2) == 1 or D == 1) and (t.stride(1) == D or H == 1),
+          f"{name}: [{T}, {H}, {D}] of {dtype} on {device} with heads side by side is needed")
+    return t.data_ptr(), t.stride(0) if T > 1 else H * D
+
+
+def qk_norm_rope(q, k=None, v=None, *, q_out, k_out=None, q_weight=None, k_weight=None, eps=1e-6, pos=None, rope=None,
+                 cache=None, table=None, seq=None, at=None, err=None, stream=None):
+    """Norm and rotation of a step's query and key heads, and the append of keys and values to a PageCache
+    (lsa_qk_norm_rope).
+
+    q [T, Hq, D], k and v [T, Hkv, D] (any stride between tokens; parts of one projection's output are fine); q_out,
+    k_out likewise, or q and k themselves.  q_weight, k_weight [D]: norm weights, None: no norm.  pos int32 [T] with
+    rope.  With cache: token t becomes entry at[t] of table row seq[t] (row t if seq is None).
+    """
+    dev = q.device
+    _need(q.dim() == 3 and q.dtype in (torch.float32, torch.bfloat16), "q: [T, Hq, D] of float32 or bfloat16 is needed")
+    T, Hq, D = q.shape
+    Hkv = 0 if k is None else k.shape[1]
+    qp, qs = _heads(q, "q", T, Hq, D, q.dtype, dev)
+    qop, qos = _heads(q_out, "q_out", T, Hq, D, q.dtype, dev)
+    kp, ks = (None, 0) if k is None else _heads(k, "k", T, Hkv, D, q.dtype, dev)
+    kop, kos = (None, 0) if k_out is None else _heads(k_out, "k_out", T, Hkv, D, q.dtype, dev)
+    vp, vs = (None, 0) if v is None else _heads(v, "v", T, Hkv, D, q.dtype, dev)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        _need(w is None or (w.dtype == q.dtype and tuple(w.shape) == (D,) and w.is_contiguous() and w.device == dev),
+              f"{name}: contiguous [{D}] of {q.dtype} on {dev} is needed")
+    _need(rope is None or rope.freq.device == dev or rope.freq.numel() == 0, "rope: freq on q's device is needed")
+    tp, ts, rows, pages = None, 0, 0, 0
+    if cache is not None:
+        _need(cache.device == dev, "cache: on q's device is needed")
+        _need(table is not None and at is not None, "a cache needs table and at")
+        tp, ts = _table_args(table, dev)
+        rows, pages = table.shape
+    _on(dev, _L.lsa_qk_norm_rope,
+        (qp, qs, qop, qos, kp, ks, kop, kos, vp, vs, _ELEM[q.dtype], T, Hq, Hkv, D, _ptr(q_weight), _ptr(k_weight),
+         eps, None if pos is None else _i32(pos, "pos", dev, (T,)), None if rope is None else rope._ref,
+         None if cache is None else cache._ref, tp, ts, rows, pages,
+         None if seq is None else _i32(seq, "seq", dev, (T,)), None if at is None else _i32(at, "at", dev, (T,)),
+         _err_word(err, dev)), "lsa_qk_norm_rope", stream)
+
+
+class PageTable:
+    """The books of a cache's pages (lsa_page_table in lsa.h): table int32 [n_rows, max_pages], len int32 [n_rows] and
+    refs int32 [n_pages], contiguous, on one device."""
+
+    def __init__(self, table, length, refs, page_size):
+        _need(table.dim() == 2, "table: [n_rows, max_pages] is needed")
+        self.table, self.len, self.refs, self.page_size = table, length, refs, int(page_size)
+        self.device = table.device
+        self.n_rows, self.max_pages = table.shape
+        self.n_pages = refs.numel()
+        self.desc = PageTableDesc(_i32(table, "table", self.device, table.shape),
+                                  _i32(length, "length", self.device, (self.n_rows,)),
+                                  _i32(refs, "refs", self.device, (self.n_pages,)), self.n_rows, self.max_pages,
+                                  self.page_size, self.n_pages)
+        self._ref = ctypes.byref(self.desc)
+
+    @classmethod
+    def empty(cls, n_rows, max_pages, n_pages, page_size, device="cuda"):
+        """Books without a held page."""
+        return cls(torch.full((n_rows, max_pages), -1, dtype=torch.int32, device=device),
+                   torch.zeros(n_rows, dtype=torch.int32, device=device),
+                   torch.zeros(n_pages, dtype=torch.int32, device=device), page_size)
+
+
+def page_grow(pages, add, err=None, stream=None):
+    """Row r of `pages` becomes add[r] entries longer and takes the pages that needs (lsa_page_grow)."""
+    _on(pages.device, _L.lsa_page_grow, (pages._ref, _i32(add, "add", pages.device, (pages.n_rows,)),
+                                         _err_word(err, pages.device)), "lsa_page_grow", stream)
+
+
+def page_fork(pages, src, dst, copy_src, copy_dst, err=None, stream=None):
+    """Row dst[i] becomes a copy of row src[i]; (copy_src, copy_dst): the pages to copy, -1 for none (lsa_page_fork)."""
+    dev, n = pages.device, src.numel()
+    _on(dev, _L.lsa_page_fork,
+        (pages._ref, _i32(src, "src", dev, (n,)), _i32(dst, "dst", dev, (n,)), n,
+         _i32(copy_src, "copy_src", dev, (n,)), _i32(copy_dst, "copy_dst", dev, (n,)), _err_word(err, dev)),
+        "lsa_page_fork", stream)
+
+
+def page_free(pages, rows, err=None, stream=None):
+    """The rows give back their pages and become empty (lsa_page_free)."""
+    _on(pages.device, _L.lsa_page_free, (pages._ref, _i32(rows, "rows", pages.device, (rows.numel(),)), rows.numel(),
+                                         _err_word(err, pages.device)), "lsa_page_free", stream)
+
+
+def page_compact_workspace_size(n_pages) -> int:
+    return int(_L.lsa_page_compact_workspace_size(n_pages))
+
+
+def page_compact(pages, table_out, refs_out, move_src, move_dst, n_moves, workspace, stream=None):
+    """Packs the held pages to the pool's front (lsa_page_compact); the moves go to page_copy of each layer's cache."""
+    dev = pages.device
+    _need(workspace.device == dev and workspace.is_contiguous(), "workspace: a contiguous tensor on the books' device")
+    _on(dev, _L.lsa_page_compact,
+        (pages._ref, _i32(table_out, "table_out", dev, pages.table.shape), _i32(refs_out, "refs_out", dev,
+                                                                               (pages.n_pages,)),
+         _i32(move_src, "move_src", dev, (pages.n_pages,)), _i32(move_dst, "move_dst", dev, (pages.n_pages,)),
+         _i32(n_moves, "n_moves", dev, (1,)), workspace.data_ptr(), workspace.numel() * workspace.element_size()),
+        "lsa_page_compact", stream)
+
+
+def page_copy(cache, src, dst, count=None, err=None, stream=None):
+    """Copies pages src[i] -> dst[i] of a PageCache (lsa_page_copy), the first `count` of them where that is given."""
+    dev, n = cache.device, src.numel()
+    _on(dev, _L.lsa_page_copy,
+        (cache._ref, _i32(src, "src", dev, (n,)), _i32(dst, "dst", dev, (n,)), n,
+         None if count is None else _i32(count, "count", dev, (1,)), _err_word(err, dev)), "lsa_page_copy", stream)
 
 
 # ----------------------------------------------------------- decode context
