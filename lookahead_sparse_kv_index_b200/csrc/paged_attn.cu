@@ -1,9 +1,10 @@
 // Attention of one new token per sequence over a paged key-value cache (lsa_paged_attn):
 //     a_t = scale q . K_t,   out = sum_t softmax(a)_t V_t,   lse = log sum_t exp(a_t).
 //
-// This file holds the entry point, the CUDA-core kernel and the combine.  paged_attn.cuh says how the work is cut.
+// This file holds the entry point, the kernel of fp32 rows and the combine; bf16 and e4m3 rows are paged_attn_mma.cu's.
+// paged_attn.cuh says how the work is cut.
 //
-// The CUDA-core kernel (fp32 products): a CTA of 8 warps stages `tile` entries of K and V at a time in shared memory
+// The kernel of fp32 rows runs on the CUDA cores (the tensor cores have no fp32 product): a CTA of 8 warps stages `tile` entries of K and V at a time in shared memory
 // through a ring of cp.async stages.  Eight lanes share an entry (each D / 8 of its elements, 16-byte pieces), so a
 // warp holds four entries; every group of eight lanes runs its own online softmax over its entries (max m, sum l and
 // o in registers) for NH query heads, the warps split first the heads and then the entries, and the parts meet once,
@@ -23,9 +24,6 @@ __device__ __forceinline__ uint32_t smem_addr(const void *p) { return uint32_t(_
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool valid) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
-}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void cp_wait(int left) {
     if (left <= 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -33,39 +31,20 @@ __device__ __forceinline__ void cp_wait(int left) {
     else asm volatile("cp.async.wait_group 2;" ::: "memory");
 }
 
-// Four consecutive elements of a staged row, in fp32.
-template <typename T>
-__device__ __forceinline__ float4 load4(const uint8_t *row, int chunk);
-template <>
-__device__ __forceinline__ float4 load4<float>(const uint8_t *row, int chunk) {
+__device__ __forceinline__ float4 load4(const uint8_t *row, int chunk) {
     return *reinterpret_cast<const float4 *>(row + chunk * 16);
-}
-template <>
-__device__ __forceinline__ float4 load4<uint16_t>(const uint8_t *row, int chunk) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(row + chunk * 8);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xffff0000u));
-}
-template <>
-__device__ __forceinline__ float4 load4<uint8_t>(const uint8_t *row, int chunk) {
-    const uint32_t u = *reinterpret_cast<const uint32_t *>(row + chunk * 4);
-    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(u & 0xffffu), __NV_E4M3);
-    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(u >> 16), __NV_E4M3);
-    const float2 a = __half22float2(__half2(lo)), b = __half22float2(__half2(hi));
-    return make_float4(a.x, a.y, b.x, b.y);
 }
 
 // KC: 4-element chunks of a lane (D <= 32 KC); NH: query heads of a warp.
-template <typename T, int KC, int NH>
+template <int KC, int NH>
 __global__ void __launch_bounds__(kThreads) paged_attn_cc(AttnArgs a, int stages, int nhg) {
-    constexpr bool kScaled = sizeof(T) == 1;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t scratch[40];
     __shared__ Entry ring[kRing][kMaxTile];
     const int D = a.cache.D, HS = a.HS, tile = a.tile;
     const bool latent = a.cache.v == a.cache.k;
-    const int row_bytes = D * int(sizeof(T)), nch = row_bytes / 16;
-    const int stage_bytes = tile * row_bytes * (latent ? 1 : 2) + (kScaled ? tile * 8 : 0);
+    const int row_bytes = D * 4, nch = row_bytes / 16;
+    const int stage_bytes = tile * row_bytes * (latent ? 1 : 2);
     float *qs = reinterpret_cast<float *>(smem + size_t(stages) * stage_bytes);   // [HS][D]
     float *po = qs + HS * D;                                                      // [TS][HS][D]
     const int TS = kWarps / nhg;
@@ -76,7 +55,7 @@ __global__ void __launch_bounds__(kThreads) paged_attn_cc(AttnArgs a, int stages
 
     pdl_launch_dependents();
     pdl_wait();
-    for_pieces<kThreads>(a, scratch, [&](int b, int hseg, int lo, int hi, int slot) {
+    for_pieces(a, scratch, [&](int b, int hseg, int lo, int hi, int slot) {
         const int kvh = hseg / a.HG, first = (hseg % a.HG) * HS;
         const int32_t *row = a.table + int64_t(b) * a.table_stride;
         const int ntiles = (hi - lo + tile - 1) / tile;
@@ -99,14 +78,6 @@ __global__ void __launch_bounds__(kThreads) paged_attn_cc(AttnArgs a, int stages
                     if (!latent)
                         cp_async16(st + (tile + r) * row_bytes + c * 16, vbase + (ok ? e.off : 0) + c * 16, ok);
                 }
-                if (kScaled && threadIdx.x < tile) {
-                    const Entry e = ring[j % kRing][threadIdx.x];
-                    const bool ok = e.off >= 0;
-                    const int64_t at = ok ? e.slot * a.cache.Hkv + kvh : 0;
-                    const uint32_t sc = st + tile * row_bytes * (latent ? 1 : 2) + threadIdx.x * 4;
-                    cp_async4(sc, a.cache.ks + at, ok);
-                    cp_async4(sc + tile * 4, a.cache.vs + at, ok);
-                }
             }
             cp_commit();
         };
@@ -117,8 +88,7 @@ __global__ void __launch_bounds__(kThreads) paged_attn_cc(AttnArgs a, int stages
             if (first + h < a.G) {
                 const int64_t at = (int64_t(kvh) * a.G + first + h) * D + d;
                 const uint8_t *q = static_cast<const uint8_t *>(a.q) + int64_t(b) * a.q_stride;
-                v = a.q_f32 ? reinterpret_cast<const float *>(q)[at]
-                            : bf16_to_f32(reinterpret_cast<const uint16_t *>(q)[at]);
+                v = reinterpret_cast<const float *>(q)[at];
             }
             qs[i] = v;
         }
@@ -141,11 +111,9 @@ __global__ void __launch_bounds__(kThreads) paged_attn_cc(AttnArgs a, int stages
             locate(i + stages);
             const uint8_t *st = smem + size_t(i % stages) * stage_bytes;
             const uint8_t *sv = latent ? st : st + tile * row_bytes;
-            const float *sc = reinterpret_cast<const float *>(st + tile * row_bytes * (latent ? 1 : 2));
             for (int t0 = ts * 4; t0 < tile; t0 += TS * 4) {
                 const int t = min(t0 + grp, tile - 1);
                 const bool ok = t0 + grp < tile && ring[i % kRing][t].off >= 0;
-                const float ks = kScaled ? sc[t] : 1.f, vs = kScaled ? sc[tile + t] : 1.f;
                 float dot[NH];
 #pragma unroll
                 for (int h = 0; h < NH; ++h) dot[h] = 0.f;
@@ -153,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) paged_attn_cc(AttnArgs a, int stages
                 for (int c = 0; c < KC; ++c) {
                     const int ch = c * 8 + dl;
                     if (ch * 4 < D) {
-                        const float4 kx = load4<T>(st + t * row_bytes, ch);
+                        const float4 kx = load4(st + t * row_bytes, ch);
 #pragma unroll
                         for (int h = 0; h < NH; ++h) {
                             const float4 q = *reinterpret_cast<const float4 *>(qs + (hw + h) * D + ch * 4);
@@ -165,26 +133,25 @@ __global__ void __launch_bounds__(kThreads) paged_attn_cc(AttnArgs a, int stages
 #pragma unroll
                 for (int c = 0; c < KC; ++c) {
                     const int ch = c * 8 + dl;
-                    vx[c] = ch * 4 < D ? load4<T>(sv + t * row_bytes, ch) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    vx[c] = ch * 4 < D ? load4(sv + t * row_bytes, ch) : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
 #pragma unroll
                 for (int h = 0; h < NH; ++h) {
                     float s = dot[h];
 #pragma unroll
                     for (int x = 1; x < 8; x <<= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-                    s = ok ? s * (ks * scale2) : -INFINITY;
+                    s = ok ? s * scale2 : -INFINITY;
                     const float mn = fmaxf(m[h], s), ref = mn == -INFINITY ? 0.f : mn;
                     const float f = exp2_approx(m[h] - ref);
                     const float p = ok ? exp2_approx(s - ref) : 0.f;
                     m[h] = mn;
                     l[h] = fmaf(l[h], f, p);
-                    const float pv = p * vs;
 #pragma unroll
                     for (int c = 0; c < KC; ++c) {
-                        o[h][c * 4] = fmaf(pv, vx[c].x, o[h][c * 4] * f);
-                        o[h][c * 4 + 1] = fmaf(pv, vx[c].y, o[h][c * 4 + 1] * f);
-                        o[h][c * 4 + 2] = fmaf(pv, vx[c].z, o[h][c * 4 + 2] * f);
-                        o[h][c * 4 + 3] = fmaf(pv, vx[c].w, o[h][c * 4 + 3] * f);
+                        o[h][c * 4] = fmaf(p, vx[c].x, o[h][c * 4] * f);
+                        o[h][c * 4 + 1] = fmaf(p, vx[c].y, o[h][c * 4 + 1] * f);
+                        o[h][c * 4 + 2] = fmaf(p, vx[c].z, o[h][c * 4 + 2] * f);
+                        o[h][c * 4 + 3] = fmaf(p, vx[c].w, o[h][c * 4 + 3] * f);
                     }
                 }
             }
@@ -242,7 +209,7 @@ __global__ void __launch_bounds__(kCombineThreads) paged_attn_combine(AttnArgs a
             if (threadIdx.x == 0 && a.lse) a.lse[hq] = -INFINITY;
         }
     }
-    const Where w = find_start<kCombineThreads>(a, c, grid, scratch);
+    const Where w = find_start(a, c, grid, scratch);
     if (w.b < 0) return;
     const int64_t n = tiles_of(a, w.b), u = int64_t(c) * w.share;
     const int hseg = int((u - w.base) / n);
@@ -305,40 +272,38 @@ AttnPlan plan_cc(const lsa_page_cache &c, int Hq) {
     const int nhg = ceil_pow2(G >= kWarps * nh ? kWarps : (G + nh - 1) / nh);
     p.HS = nhg * nh;
     p.HG = (G + p.HS - 1) / p.HS;
-    const size_t entry = size_t(c.D) * elem_size(c.dtype) * (c.v == c.k ? 1 : 2) + (c.dtype == LSA_E4M3 ? 8 : 0);
+    const size_t entry = size_t(c.D) * 4 * (c.v == c.k ? 1 : 2);
     p.tile = kMaxTile;
     while (p.tile > 4 && p.tile * entry > 24 * 1024) p.tile /= 2;
     p.stages = 4;
     p.threads = kThreads;
     p.smem = p.stages * p.tile * entry + (size_t(p.HS) * c.D + size_t(kWarps / nhg) * p.HS * (c.D + 2)) * 4;
     p.grid = sm_count() * 2;
-    p.ok = true;
     return p;
 }
 
-template <typename T, int KC, int NH>
+template <int KC, int NH>
 lsa_status launch_cc(const AttnArgs &a, const AttnPlan &p, int grid, cudaStream_t st) {
-    LSA_CUDA(ensure_smem(paged_attn_cc<T, KC, NH>, p.smem));
-    LSA_CUDA(launch_pdl(paged_attn_cc<T, KC, NH>, dim3(grid), dim3(kThreads), p.smem, st, a, int(p.stages),
+    LSA_CUDA(ensure_smem(paged_attn_cc<KC, NH>, p.smem));
+    LSA_CUDA(launch_pdl(paged_attn_cc<KC, NH>, dim3(grid), dim3(kThreads), p.smem, st, a, int(p.stages),
                         int(p.HS / NH)));
     LSA_LAUNCHED("paged_attn_cc");
     return LSA_OK;
 }
 
-template <typename T>
 lsa_status dispatch_cc(const AttnArgs &a, const AttnPlan &p, int grid, cudaStream_t st) {
     switch (cc_chunks(a.cache.D)) {
-    case 1: return launch_cc<T, 1, 8>(a, p, grid, st);
-    case 2: return launch_cc<T, 2, 8>(a, p, grid, st);
-    case 3: return launch_cc<T, 3, 4>(a, p, grid, st);
-    case 4: return launch_cc<T, 4, 4>(a, p, grid, st);
-    case 6: return launch_cc<T, 6, 2>(a, p, grid, st);
-    case 8: return launch_cc<T, 8, 2>(a, p, grid, st);
-    default: return launch_cc<T, 16, 1>(a, p, grid, st);
+    case 1: return launch_cc<1, 8>(a, p, grid, st);
+    case 2: return launch_cc<2, 8>(a, p, grid, st);
+    case 3: return launch_cc<3, 4>(a, p, grid, st);
+    case 4: return launch_cc<4, 4>(a, p, grid, st);
+    case 6: return launch_cc<6, 2>(a, p, grid, st);
+    case 8: return launch_cc<8, 2>(a, p, grid, st);
+    default: return launch_cc<16, 1>(a, p, grid, st);
     }
 }
 
-AttnPlan plan_of(const lsa_page_cache &c, int Hq) { return plan_cc(c, Hq); }
+AttnPlan plan_of(const lsa_page_cache &c, int Hq) { return c.dtype == LSA_F32 ? plan_cc(c, Hq) : plan_mma(c, Hq); }
 
 // A segment of so few units is done by one CTA, without partials and a second launch.
 constexpr int kWholeUnits = 8;
@@ -464,9 +429,7 @@ extern "C" lsa_status lsa_paged_attn(const void *Q, lsa_dtype q_dtype, int64_t q
     a.whole = most <= int64_t(kWholeUnits) * p.tile && segments < (int64_t(1) << 31);
     const int grid = a.whole ? int(segments) : p.grid;
     cudaStream_t st = as_stream(stream);
-    if (cache->dtype == LSA_F32) s = dispatch_cc<float>(a, p, grid, st);
-    else if (cache->dtype == LSA_BF16) s = dispatch_cc<uint16_t>(a, p, grid, st);
-    else s = dispatch_cc<uint8_t>(a, p, grid, st);
+    s = cache->dtype == LSA_F32 ? dispatch_cc(a, p, grid, st) : launch_mma(*cache, a, p, grid, st);
     if (s != LSA_OK || a.whole) return s;
     return paged_combine(a, grid, st);
 }

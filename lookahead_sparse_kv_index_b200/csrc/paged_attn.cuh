@@ -64,11 +64,10 @@ struct Where {
 };
 
 // Finds the owner of unit `grid index * share` (whole block; `scratch`: 40 int64 of shared memory).
-template <int THREADS>
-__device__ Where find_start(const AttnArgs &a, int64_t cta, int64_t grid, int64_t *scratch) {
-    constexpr int kWarps = THREADS / 32;
+__device__ inline Where find_start(const AttnArgs &a, int64_t cta, int64_t grid, int64_t *scratch) {
+    const int threads = blockDim.x, warps = threads >> 5;
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    const int per = (a.B + THREADS - 1) / THREADS;
+    const int per = (a.B + threads - 1) / threads;
     const int b0 = min(a.B, t * per), b1 = min(a.B, b0 + per);
     int64_t mine = 0;
     for (int b = b0; b < b1; ++b) mine += tiles_of(a, b);
@@ -82,7 +81,7 @@ __device__ Where find_start(const AttnArgs &a, int64_t cta, int64_t grid, int64_
     if (t == 0) scratch[34] = -1;
     __syncthreads();
     int64_t before = 0, total = 0;
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < warps; ++w) {
         if (w < warp) before += scratch[w];
         total += scratch[w];
     }
@@ -128,7 +127,7 @@ __device__ __forceinline__ Entry entry_at(const AttnArgs &a, const int32_t *row,
 
 // The pieces of a CTA, in unit order: f(b, hseg, lo, hi, slot) for entries [lo, hi) of sequence b and segment hseg (kv
 // head hseg / HG, head group hseg % HG); slot: where the piece's partial goes, -1 where the piece is a whole segment.
-template <int THREADS, typename F>
+template <typename F>
 __device__ __forceinline__ void for_pieces(const AttnArgs &a, int64_t *scratch, F f) {
     const int heads = a.cache.Hkv * a.HG;
     if (a.whole) {
@@ -137,7 +136,7 @@ __device__ __forceinline__ void for_pieces(const AttnArgs &a, int64_t *scratch, 
         f(b, int(blockIdx.x) - b * heads, s.lo, s.hi, -1);
         return;
     }
-    const Where w = find_start<THREADS>(a, blockIdx.x, gridDim.x, scratch);
+    const Where w = find_start(a, blockIdx.x, gridDim.x, scratch);
     if (w.b < 0) return;
     int b = w.b;
     int64_t base = w.base, u = int64_t(blockIdx.x) * w.share;
@@ -205,8 +204,10 @@ __device__ __forceinline__ void finish_piece(const AttnArgs &a, int b, int hseg,
 struct AttnPlan {
     int32_t HG, HS, tile, grid, threads, stages;
     size_t smem;
-    bool ok;
 };
+// bf16 and e4m3 rows: the tensor-core kernel (paged_attn_mma.cu).
+AttnPlan plan_mma(const lsa_page_cache &c, int Hq);
+lsa_status launch_mma(const lsa_page_cache &c, const AttnArgs &a, const AttnPlan &p, int grid, cudaStream_t st);
 lsa_status paged_combine(const AttnArgs &a, int grid, cudaStream_t st);
 
 }  // namespace paged

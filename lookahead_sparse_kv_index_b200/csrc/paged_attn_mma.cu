@@ -1,0 +1,568 @@
+// Attention of one new token over a paged cache, on the tensor cores (bf16 and e4m3 rows; paged_attn.cuh says how the
+// work is cut).
+//
+// One new token per sequence makes S = q K^T a product with as few rows as query heads share a kv head (1 .. 32), so
+// the entries take the 16-row side of mma.m16n8k16 and the heads its 8-column side: S^T = K q^T, then O^T = V^T P^T.
+// Nothing of it is near the tensor rate; what bounds the kernel is HBM, and the layout serves that:
+//   * every warp is a pipeline of its own: it copies steps of 16 or 32 entries (8 KB of K and V rows at a head dim of
+//     128 bf16) through `stages` cp.async stages and never waits for another warp before the end of a piece;
+//   * K is read from shared memory 16 bytes a lane, straight into A fragments: which 8 (16 for e4m3) elements of a head
+//     dim are a fragment's k index is a free choice as long as q's fragment makes the same one;
+//   * V^T needs pairs of entries side by side for one element: a lane reads 16 bytes of four entries' rows and byte
+//     permutes pair them; the entry of each fragment index is chosen (entry_of) so that neither read has bank conflicts;
+//   * P^T leaves the accumulators with entries along its rows and has to enter with entries along k: one 8 x 8
+//     movmatrix transpose a tile.
+// Types.  bf16 rows are multiplied as they are.  e4m3 rows become f16 (exactly); q becomes f16 times a power of two of
+// its own head, which is exact for elements down to 2^-28 of the head's largest and off by less than 2^-38 of it below;
+// the scales of K multiply the fp32 scores, those of V the weights before they are rounded, relative to the largest
+// scale 2^R so far (o is rescaled when R grows, as it is when the running max does).
+// A weight is rounded to 16 bits for its product with V and the rest rounded again, so it enters as a sum of two 16-bit
+// numbers (within 2^-17 for bf16): with one, its rounding is as large as the output's own and showed in the result.
+#include "paged_attn.cuh"
+
+namespace lsa {
+namespace paged {
+namespace {
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) { return uint32_t(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool valid) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_wait(int left) {
+    if (left <= 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else if (left == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 2;" ::: "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ float lds_f(uint32_t at) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+// Two e4m3 values (low 16 bits; high 16 bits) to two f16.
+__device__ __forceinline__ void e4m3_to_f16(uint32_t x, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x));
+}
+template <bool F16>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    if constexpr (F16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%0, %1, %2, %3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+                     "{%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Two weights as 16-bit numbers, and what their rounding left as two more.
+template <bool F16>
+__device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &lo) {
+    if constexpr (F16) {
+        const __half2 h = __floats2half2_rn(x, y);
+        const float2 f = __half22float2(h);
+        const __half2 r = __floats2half2_rn(x - f.x, y - f.y);
+        hi = *reinterpret_cast<const uint32_t *>(&h);
+        lo = *reinterpret_cast<const uint32_t *>(&r);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        const float2 f = __bfloat1622float2(h);
+        const __nv_bfloat162 r = __floats2bfloat162_rn(x - f.x, y - f.y);
+        hi = *reinterpret_cast<const uint32_t *>(&h);
+        lo = *reinterpret_cast<const uint32_t *>(&r);
+    }
+}
+
+// Staged row of fragment index r (0 .. 15).  With rows an odd number of 16-byte pieces apart, or their pieces permuted
+// by the row's low bits, the rows of indices (2j, 2j + 1) lie 4 pieces apart and those of (0, 2, 4, 6), (1, 3, 5, 7)
+// and so on 2 apart: the eight lanes of a 16-byte read phase (two rows x four pieces for K, four rows x two pieces for
+// V) meet eight different bank groups.
+__device__ __forceinline__ int entry_of(int r) {
+    const int j = (r >> 1) & 3, hi = r >> 3;
+    return r & 1 ? 8 + ((2 * j + 4) & 7) + hi : 2 * j + hi;
+}
+
+// A shape of the kernel.  KB: 64-byte blocks of a row; NT: groups of 8 query heads.
+template <bool E4M3, int KB, int NT>
+struct Shape {
+    static constexpr int kPieces = KB * 4;                              // 16-byte pieces of a staged row
+    static constexpr bool kSwizzle = kPieces % 8 == 0;
+    static constexpr int kPitch = (kSwizzle ? kPieces : kPieces + 1) * 16;
+    static constexpr int kM = KB <= 2 ? 2 : 1;                          // 16-entry tiles of a step
+    static constexpr int kStep = 16 * kM;
+    static constexpr int kElems = E4M3 ? 16 : 8;                        // elements of a piece
+    static constexpr int kPass = (kPieces + 7) / 8;                     // 8-piece passes over a V row
+    static constexpr int kTiles = kElems / 2;                           // O^T tiles of a pass
+    static constexpr int kQPer = E4M3 ? 2 : 1;                          // 16-byte q fragments of a block and head group
+    static constexpr bool kQInRegs = KB * NT * kQPer * 4 <= 32;
+    static constexpr int kQBytes = KB * NT * kQPer * 512;
+    static constexpr int kRows = kStep * kPitch;                        // bytes of a stage's K (or V) rows
+    static constexpr int kTail = 16 + (E4M3 ? kStep * 8 : 0);           // entry mask, scales
+    static constexpr int kHeads = 8 * NT;
+    __host__ __device__ static constexpr int stage(bool latent) { return kRows * (latent ? 1 : 2) + kTail; }
+};
+
+constexpr int kMaxWarps = 4;
+
+template <bool E4M3, int KB, int NT>
+__global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int stages) {
+    using C = Shape<E4M3, KB, NT>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int64_t scratch[40];
+    __shared__ float q_scale[C::kHeads];
+    const int D = a.cache.D, nch = D / C::kElems;
+    const bool latent = a.cache.v == a.cache.k;
+    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int stage_bytes = C::stage(latent), v_at = latent ? 0 : C::kRows;
+    const uint32_t mine = smem_addr(smem) + C::kQBytes + warp * stages * stage_bytes;
+    const uint32_t qf = smem_addr(smem);
+    // where the parts of a piece meet, over the stages
+    float *po = reinterpret_cast<float *>(smem + C::kQBytes);
+    float *pml = po + size_t(warps) * C::kHeads * D;
+    const float scale2 = a.scale * kLog2e;
+
+    auto piece_at = [](int row, int p) { return row * C::kPitch + ((C::kSwizzle ? p ^ (row & 7) : p) << 4); };
+
+    pdl_launch_dependents();
+    pdl_wait();
+    auto do_piece = [&](int b, int hseg, int lo, int hi, int slot) {
+        const int kvh = hseg / a.HG, first = (hseg % a.HG) * C::kHeads;
+        const int32_t *row = a.table + int64_t(b) * a.table_stride;
+        const uint8_t *kbase = a.cache.k + kvh * a.cache.head_stride, *vbase = a.cache.v + kvh * a.cache.head_stride;
+        const int steps = (hi - lo + C::kStep - 1) / C::kStep;
+        const int n = steps > warp ? (steps - warp + warps - 1) / warps : 0;   // of this warp: warp, warp + warps, ...
+
+        auto locate = [&](int j) {
+            const int t = lo + (warp + j * warps) * C::kStep + lane;
+            return j < n && lane < C::kStep && t < hi ? entry_at(a, row, t) : Entry{-1, 0};
+        };
+        auto issue = [&](int j, const Entry &e) {
+            if (j < n) {
+                const uint32_t st = mine + (j % stages) * stage_bytes;
+#pragma unroll
+                for (int i = 0; i < C::kStep * C::kPieces / 32; ++i) {
+                    const int r = (i * 32 + lane) / C::kPieces, p = (i * 32 + lane) % C::kPieces;
+                    const int64_t off = __shfl_sync(0xffffffffu, e.off, r);
+                    const bool ok = off >= 0 && p < nch;
+                    const int64_t from = ok ? off + p * 16 : 0;
+                    cp_async16(st + piece_at(r, p), kbase + from, ok);
+                    if (!latent) cp_async16(st + v_at + piece_at(r, p), vbase + from, ok);
+                }
+                const uint32_t tail = st + v_at + C::kRows;
+                const uint32_t mask = __ballot_sync(0xffffffffu, e.off >= 0);
+                if (lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(tail), "r"(mask) : "memory");
+                if (E4M3 && lane < C::kStep) {
+                    const bool ok = e.off >= 0;
+                    const int64_t at = ok ? e.slot * a.cache.Hkv + kvh : 0;
+                    cp_async4(tail + 16 + lane * 4, a.cache.ks + at, ok);
+                    cp_async4(tail + 16 + (C::kStep + lane) * 4, a.cache.vs + at, ok);
+                }
+            }
+            cp_commit();
+        };
+
+        Entry ahead = locate(0);
+        for (int j = 0; j < stages - 1; ++j) {
+            issue(j, ahead);
+            ahead = locate(j + 1);
+        }
+
+        // q fragments of the piece's heads: lane (g, c) of block kb and head group nt holds head 8 nt + g, piece 4 kb + c
+        {
+            const uint16_t *q = reinterpret_cast<const uint16_t *>(static_cast<const uint8_t *>(a.q) +
+                                                                   int64_t(b) * a.q_stride) +
+                                (int64_t(kvh) * a.G + first) * D;
+            if constexpr (E4M3) {
+                for (int h = warp; h < C::kHeads; h += warps) {
+                    float m = 0.f;
+                    if (first + h < a.G)
+                        for (int d = lane; d < D; d += 32) m = fmaxf(m, fabsf(bf16_to_f32(q[int64_t(h) * D + d])));
+#pragma unroll
+                    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+                    // 2^(13 - exponent): the largest element comes to lie in [2^13, 2^14)
+                    int e = int(__float_as_uint(m) >> 23) - 127;
+                    e = m == 0.f || e == 128 ? 13 : e < -110 ? -110 : e;
+                    if (lane == 0) q_scale[h] = __uint_as_float(uint32_t(127 + 13 - e) << 23);
+                }
+                __syncthreads();
+            }
+            for (int i = threadIdx.x; i < KB * NT * 32; i += blockDim.x) {
+                const int l = i & 31, nt = (i >> 5) % NT, kb = (i >> 5) / NT;
+                const int h = nt * 8 + (l >> 2), p = kb * 4 + (l & 3);
+                const bool ok = first + h < a.G && p < nch;
+                uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                if (ok) {
+#pragma unroll
+                    for (int x = 0; x < C::kQPer; ++x)
+                        v[x] = *reinterpret_cast<const uint4 *>(q + int64_t(h) * D + p * C::kElems + 8 * x);
+                }
+                if constexpr (E4M3) {
+                    const float f = q_scale[h];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        uint32_t *w = reinterpret_cast<uint32_t *>(&v[x]);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const __half2 t = __floats2half2_rn(__uint_as_float(w[y] << 16) * f,
+                                                                __uint_as_float(w[y] & 0xffff0000u) * f);
+                            w[y] = *reinterpret_cast<const uint32_t *>(&t);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < C::kQPer; ++x)
+                    *reinterpret_cast<uint4 *>(smem + ((size_t(kb) * NT + nt) * C::kQPer + x) * 512 + l * 16) = v[x];
+            }
+        }
+        __syncthreads();
+        uint4 qr[C::kQInRegs ? KB * NT * C::kQPer : 1];
+        if constexpr (C::kQInRegs) {
+#pragma unroll
+            for (int i = 0; i < KB * NT * C::kQPer; ++i) qr[i] = lds16(qf + i * 512 + lane * 16);
+        }
+        float sf[NT][2];      // score factor of heads 8 nt + 2c, + 1
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) sf[nt][x] = E4M3 ? scale2 / q_scale[nt * 8 + 2 * c + x] : scale2;
+
+        float m[NT][2], l[NT][2], o[C::kPass][C::kTiles][NT][4];
+        int R = -100;         // weights are held relative to scales of 2^R (e4m3)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+            for (int p = 0; p < C::kPass; ++p)
+#pragma unroll
+                for (int t = 0; t < C::kTiles; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[p][t][nt][e] = 0.f;
+        }
+
+        for (int j = 0; j < n; ++j) {
+            cp_wait(stages - 2);
+            __syncwarp();
+            issue(j + stages - 1, ahead);
+            ahead = locate(j + stages);
+            const uint32_t st = mine + (j % stages) * stage_bytes, sv = st + v_at, tail = sv + C::kRows;
+            uint32_t mask;
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(mask) : "r"(tail));
+
+            float s[C::kM][NT][4];
+#pragma unroll
+            for (int tm = 0; tm < C::kM; ++tm)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[tm][nt][e] = 0.f;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                uint4 q[NT][C::kQPer];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < C::kQPer; ++x)
+                        q[nt][x] = C::kQInRegs ? qr[C::kQInRegs ? (kb * NT + nt) * C::kQPer + x : 0]
+                                               : lds16(qf + ((kb * NT + nt) * C::kQPer + x) * 512 + lane * 16);
+#pragma unroll
+                for (int tm = 0; tm < C::kM; ++tm) {
+                    const uint4 k0 = lds16(st + piece_at(tm * 16 + entry_of(g), kb * 4 + c));
+                    const uint4 k1 = lds16(st + piece_at(tm * 16 + entry_of(g + 8), kb * 4 + c));
+                    if constexpr (E4M3) {
+                        const uint32_t u0[4] = {k0.x, k0.y, k0.z, k0.w}, u1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t a0, a1, a2, a3;
+                            e4m3_to_f16(u0[i], a0, a2);
+                            e4m3_to_f16(u1[i], a1, a3);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                const uint4 qq = q[nt][i >> 1];
+                                mma<true>(s[tm][nt], a0, a1, a2, a3, i & 1 ? qq.z : qq.x, i & 1 ? qq.w : qq.y);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma<false>(s[tm][nt], k0.x, k1.x, k0.y, k1.y, q[nt][0].x, q[nt][0].y);
+                            mma<false>(s[tm][nt], k0.z, k1.z, k0.w, k1.w, q[nt][0].z, q[nt][0].w);
+                        }
+                    }
+                }
+            }
+
+            // scores in units of log2; entries that are not there get -infinity
+            float vs[C::kM][2];
+#pragma unroll
+            for (int tm = 0; tm < C::kM; ++tm) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int r = tm * 16 + entry_of(g + 8 * y);
+                    const bool ok = (mask >> r) & 1u;
+                    const float ks = E4M3 ? lds_f(tail + 16 + r * 4) : 1.f;
+                    vs[tm][y] = E4M3 ? lds_f(tail + 16 + (C::kStep + r) * 4) : 1.f;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            float &v = s[tm][nt][2 * y + x];
+                            v = ok ? v * (E4M3 ? ks * sf[nt][x] : sf[nt][x]) : -INFINITY;
+                        }
+                }
+            }
+            int grown = 0;
+            if constexpr (E4M3) {
+                int e = -100;
+#pragma unroll
+                for (int tm = 0; tm < C::kM; ++tm)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) e = max(e, int(__float_as_uint(vs[tm][y]) >> 23 & 255) - 127);
+                e = min(__reduce_max_sync(0xffffffffu, e), 127);
+                grown = e > R ? e - R : 0;
+                R += grown;
+                const float f = __uint_as_float(uint32_t(127 + 13 - R) << 23);   // 2^(13 - R): weights of up to 2^14
+#pragma unroll
+                for (int tm = 0; tm < C::kM; ++tm) vs[tm][0] *= f, vs[tm][1] *= f;
+            }
+            float ref[NT][2], alpha[NT][2];
+            bool moved = grown != 0;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float v = -INFINITY;
+#pragma unroll
+                    for (int tm = 0; tm < C::kM; ++tm) v = fmaxf(v, fmaxf(s[tm][nt][x], s[tm][nt][2 + x]));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                    const float mn = fmaxf(m[nt][x], v);
+                    moved |= mn > m[nt][x];
+                    ref[nt][x] = mn == -INFINITY ? 0.f : mn;
+                    alpha[nt][x] = exp2_approx(m[nt][x] - ref[nt][x]);
+                    m[nt][x] = mn;
+                    l[nt][x] *= alpha[nt][x];
+                }
+            if (__any_sync(0xffffffffu, moved)) {
+                const float f = E4M3 ? __uint_as_float(uint32_t(max(127 - grown, 0)) << 23) : 1.f;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float f0 = alpha[nt][0] * f, f1 = alpha[nt][1] * f;
+#pragma unroll
+                    for (int p = 0; p < C::kPass; ++p)
+#pragma unroll
+                        for (int t = 0; t < C::kTiles; ++t) {
+                            o[p][t][nt][0] *= f0;
+                            o[p][t][nt][1] *= f1;
+                            o[p][t][nt][2] *= f0;
+                            o[p][t][nt][3] *= f1;
+                        }
+                }
+            }
+            uint32_t ph[C::kM][NT][2], pl[C::kM][NT][2];
+#pragma unroll
+            for (int tm = 0; tm < C::kM; ++tm)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        float p0 = exp2_approx(s[tm][nt][2 * y] - ref[nt][0]);
+                        float p1 = exp2_approx(s[tm][nt][2 * y + 1] - ref[nt][1]);
+                        l[nt][0] += p0;
+                        l[nt][1] += p1;
+                        if constexpr (E4M3) p0 *= vs[tm][y], p1 *= vs[tm][y];
+                        uint32_t h, r;
+                        split<E4M3>(p0, p1, h, r);
+                        ph[tm][nt][y] = movmatrix(h);
+                        pl[tm][nt][y] = movmatrix(r);
+                    }
+#pragma unroll
+            for (int p = 0; p < C::kPass; ++p) {
+#pragma unroll
+                for (int tm = 0; tm < C::kM; ++tm) {
+                    uint4 v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = tm * 16 + entry_of(2 * c + (i & 1) + 8 * (i >> 1));
+                        v[i] = p * 8 + 7 < C::kPieces || p * 8 + g < C::kPieces ? lds16(sv + piece_at(r, p * 8 + g))
+                                                                             : make_uint4(0, 0, 0, 0);
+                    }
+                    const uint32_t v0[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, v1[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
+                    const uint32_t v8[4] = {v[2].x, v[2].y, v[2].z, v[2].w}, v9[4] = {v[3].x, v[3].y, v[3].z, v[3].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (E4M3) {
+                            // bytes (e, e') of two entries: elements 4i, 4i + 1, then 4i + 2, 4i + 3
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const uint32_t sel = y ? 0x7362 : 0x5140;
+                                uint32_t a0, a1, a2, a3;
+                                e4m3_to_f16(prmt(v0[i], v1[i], sel), a0, a1);
+                                e4m3_to_f16(prmt(v8[i], v9[i], sel), a2, a3);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    float(&d)[4] = o[p][C::kTiles == 8 ? 2 * i + y : i][nt];
+                                    mma<true>(d, a0, a1, a2, a3, ph[tm][nt][0], ph[tm][nt][1]);
+                                    mma<true>(d, a0, a1, a2, a3, pl[tm][nt][0], pl[tm][nt][1]);
+                                }
+                            }
+                        } else {
+                            const uint32_t a0 = prmt(v0[i], v1[i], 0x5410), a1 = prmt(v0[i], v1[i], 0x7632);
+                            const uint32_t a2 = prmt(v8[i], v9[i], 0x5410), a3 = prmt(v8[i], v9[i], 0x7632);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                mma<false>(o[p][i][nt], a0, a1, a2, a3, ph[tm][nt][0], ph[tm][nt][1]);
+                                mma<false>(o[p][i][nt], a0, a1, a2, a3, pl[tm][nt][0], pl[tm][nt][1]);
+                            }
+                        }
+                    }
+                }
+            }
+        }
+        cp_wait(0);
+        __syncthreads();      // the parts overlay every warp's stages
+        const float back = E4M3 ? __uint_as_float(uint32_t(127 - 13 + R) << 23) : 1.f;   // 2^(R - 13)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int h = nt * 8 + 2 * c + x;
+                float L = l[nt][x];
+                L += __shfl_xor_sync(0xffffffffu, L, 4);
+                L += __shfl_xor_sync(0xffffffffu, L, 8);
+                L += __shfl_xor_sync(0xffffffffu, L, 16);
+                if (g == 0) {
+                    pml[(warp * C::kHeads + h) * 2] = m[nt][x];
+                    pml[(warp * C::kHeads + h) * 2 + 1] = L;
+                }
+#pragma unroll
+                for (int p = 0; p < C::kPass; ++p)
+#pragma unroll
+                    for (int t = 0; t < C::kTiles; ++t) {
+                        const int d = (p * 8 + g) * C::kElems + 2 * t;
+                        if (d < D)
+                            *reinterpret_cast<float2 *>(po + (size_t(warp) * C::kHeads + h) * D + d) =
+                                make_float2(o[p][t][nt][x] * back, o[p][t][nt][2 + x] * back);
+                    }
+            }
+        __syncthreads();
+        finish_piece(a, b, hseg, slot, warps, po, pml);
+        __syncthreads();
+    };
+    for_pieces(a, scratch, do_piece);
+    if (blockIdx.x == 0 && a.err)
+        for (int b = threadIdx.x; b < a.B; b += blockDim.x)
+            if (a.seq_len[b] > a.reach) raise_err(a.err, LSA_ERR_CAPACITY);
+}
+
+int blocks_of(const lsa_page_cache &c) {
+    const int need = int((size_t(c.D) * elem_size(c.dtype) + 63) / 64);
+    for (int k : {1, 2, 3, 4, 6, 8})
+        if (need <= k) return k;
+    return 16;
+}
+
+template <bool E4M3, int KB, int NT>
+struct Run {
+    static void plan(bool latent, int D, AttnPlan &p) {
+        using C = Shape<E4M3, KB, NT>;
+        const int stage = C::stage(latent);
+        // two CTAs of four warps on an SM while three stages fit; else one, then one of two warps
+        int warps = 4, ctas = 2;
+        auto fit = [&](int budget) { return (budget - C::kQBytes) / (warps * stage); };
+        int stages = fit(112 * 1024);
+        if (stages < 3) {
+            ctas = 1;
+            stages = fit(222 * 1024);
+            if (stages < 2) {
+                warps = 2;
+                stages = fit(222 * 1024);
+            }
+        }
+        p.stages = stages > 4 ? 4 : stages;
+        p.threads = warps * 32;
+        p.tile = C::kStep * warps;
+        p.grid = sm_count() * ctas;
+        const size_t ring = size_t(p.stages) * warps * stage, join = size_t(warps) * C::kHeads * (D + 2) * 4;
+        p.smem = C::kQBytes + (ring > join ? ring : join);
+    }
+    static lsa_status launch(const AttnArgs &a, const AttnPlan &p, int grid, cudaStream_t st) {
+        LSA_CUDA(ensure_smem(paged_attn_mma<E4M3, KB, NT>, p.smem));
+        LSA_CUDA(launch_pdl(paged_attn_mma<E4M3, KB, NT>, dim3(grid), dim3(p.threads), p.smem, st, a, int(p.stages)));
+        LSA_LAUNCHED(E4M3 ? "paged_attn_mma e4m3" : "paged_attn_mma bf16");
+        return LSA_OK;
+    }
+};
+
+// Calls f with the kernel's shape: Run<type, blocks of a row, head groups>.
+template <bool E4M3, int KB, typename F>
+auto with_heads(int nt, F f) {
+    constexpr int kMost = (E4M3 ? KB * 64 : KB * 32) <= 128 ? 4 : (E4M3 ? KB * 64 : KB * 32) <= 256 ? 2 : 1;
+    if constexpr (kMost >= 4)
+        if (nt > 2) return f(Run<E4M3, KB, 4>());
+    if constexpr (kMost >= 2)
+        if (nt > 1) return f(Run<E4M3, KB, 2>());
+    return f(Run<E4M3, KB, 1>());
+}
+template <bool E4M3, typename F>
+auto with_shape(int kb, int nt, F f) {
+    switch (kb) {
+    case 1: return with_heads<E4M3, 1>(nt, f);
+    case 2: return with_heads<E4M3, 2>(nt, f);
+    case 3: return with_heads<E4M3, 3>(nt, f);
+    case 4: return with_heads<E4M3, 4>(nt, f);
+    case 6: return with_heads<E4M3, 6>(nt, f);
+    case 8: return with_heads<E4M3, 8>(nt, f);
+    default:
+        // (e4m3 rows end at 8 blocks)
+        return with_heads<E4M3, E4M3 ? 8 : 16>(nt, f);
+    }
+}
+
+}  // namespace
+
+AttnPlan plan_mma(const lsa_page_cache &c, int Hq) {
+    AttnPlan p = {};
+    const int G = Hq / c.Hkv, kb = blocks_of(c), width = kb * (c.dtype == LSA_E4M3 ? 64 : 32);
+    const int most = width <= 128 ? 32 : width <= 256 ? 16 : 8;   // query heads whose o fits in registers
+    p.HG = (G + most - 1) / most;
+    const int per = (G + p.HG - 1) / p.HG, nt = per <= 8 ? 1 : per <= 16 ? 2 : 4;
+    p.HS = 8 * nt;
+    p.HG = (G + p.HS - 1) / p.HS;
+    const bool latent = c.v == c.k;
+    auto f = [&](auto run) { run.plan(latent, c.D, p); };
+    if (c.dtype == LSA_E4M3) with_shape<true>(kb, nt, f);
+    else with_shape<false>(kb, nt, f);
+    return p;
+}
+
+lsa_status launch_mma(const lsa_page_cache &c, const AttnArgs &a, const AttnPlan &p, int grid, cudaStream_t st) {
+    const int kb = blocks_of(c), nt = p.HS / 8;
+    auto f = [&](auto run) { return run.launch(a, p, grid, st); };
+    return c.dtype == LSA_E4M3 ? with_shape<true>(kb, nt, f) : with_shape<false>(kb, nt, f);
+}
+
+}  // namespace paged
+}  // namespace lsa
