@@ -211,11 +211,12 @@ __global__ void __launch_bounds__(kCombineThreads) paged_attn_combine(AttnArgs a
     }
     const Where w = find_start(a, c, grid, scratch);
     if (w.b < 0) return;
-    const int64_t n = tiles_of(a, w.b), u = int64_t(c) * w.share;
-    const int hseg = int((u - w.base) / n);
+    const int64_t n = units_of(a, w.b);
+    const int hseg = int((int64_t(c) * w.share - w.base) / n);
     const int64_t s0 = w.base + hseg * n;
-    const int64_t c0 = s0 / w.share, c1 = (s0 + n - 1) / w.share;
-    if (u == s0 || c != c0 + 1) return;
+    // the CTAs with the segment's first and last entries
+    const int64_t c0 = (s0 + a.lead) / w.share, c1 = (s0 + n - 1) / w.share;
+    if (c != c0 + 1 || c > c1) return;
     const int in = (hseg % a.HG) * HS + h;
     if (in >= a.G) return;
     const int P = int(c1 - c0) + 1;
@@ -275,6 +276,7 @@ AttnPlan plan_cc(const lsa_page_cache &c, int Hq) {
     const size_t entry = size_t(c.D) * 4 * (c.v == c.k ? 1 : 2);
     p.tile = kMaxTile;
     while (p.tile > 4 && p.tile * entry > 24 * 1024) p.tile /= 2;
+    p.lead = 2;
     p.stages = 4;
     p.threads = kThreads;
     p.smem = p.stages * p.tile * entry + (size_t(p.HS) * c.D + size_t(kWarps / nhg) * p.HS * (c.D + 2)) * 4;
@@ -422,7 +424,7 @@ extern "C" lsa_status lsa_paged_attn(const void *Q, lsa_dtype q_dtype, int64_t q
     a.part_ml = a.part_o + int64_t(p.grid) * 2 * p.HS * cache->D;
     a.err = err;
     a.tile = p.tile;
-    a.min_share = 1;
+    a.lead = p.lead;
     a.q_f32 = q_dtype == LSA_F32;
     const int64_t most = window > 0 && window < a.reach ? window : a.reach;
     const int64_t segments = int64_t(B) * cache->Hkv * p.HG;

@@ -1,10 +1,11 @@
 // Attention of one new token over a paged cache: what its two kernels and the combine share.
 //
-// The work is cut into units of `tile` entries of one segment: a segment is one sequence's one group of up to `HS`
-// query heads of a kv head.  Units are numbered sequence by sequence, head group by head group, and CTA c of the
-// grid owns the `share` consecutive units from c * share on, so every SM reads the same number of entries whatever
-// the sequences' lengths are.  A segment that lies in one CTA's share is finished there; of the others each CTA
-// writes a partial (unnormalised o, and the running max m and sum l of its softmax, both for 2^x), and the combine
+// The work is cut into units.  A segment is one sequence's one group of up to `HS` query heads of a kv head; it has
+// `lead` units for what starting and ending it costs, then one for each `tile` entries.  Units are numbered sequence
+// by sequence, head group by head group, and CTA c of the grid owns the `share` consecutive units from c * share on,
+// so every SM gets the same work whatever the sequences' lengths are (without the leading units a CTA that met many
+// short sequences took twice as long as the others: 198 us against 105 for a ragged batch of 64 sequences of 0 to
+// 16384 entries).  A segment whose entries lie in one CTA's share is finished there; of the others each CTA writes a partial (unnormalised o, and the running max m and sum l of its softmax, both for 2^x), and the combine
 // kernel joins a segment's partials in unit order:
 //     M = max m_c,  L = sum l_c 2^(m_c - M),  o = sum o_c 2^(m_c - M) / L,  lse = (M + log2 L) ln 2.
 // A CTA has at most two partials: slot 2c for the piece that continues a segment, 2c + 1 for one that begins it.
@@ -31,7 +32,7 @@ struct AttnArgs {
     float *lse;
     float *part_o, *part_ml;     // [2 * grid][HS][D], [2 * grid][HS][2]
     int32_t *err;
-    int32_t tile, min_share;
+    int32_t tile, lead;
     int32_t whole;               // 1: CTA c does segment c and no partials are written
     int32_t q_f32;
 };
@@ -56,6 +57,11 @@ __device__ __forceinline__ int32_t tiles_of(const AttnArgs &a, int b) {
     return (s.hi - s.lo + a.tile - 1) / a.tile;
 }
 
+__device__ __forceinline__ int32_t units_of(const AttnArgs &a, int b) {
+    const int32_t n = tiles_of(a, b);
+    return n ? n + a.lead : 0;
+}
+
 // Where a unit lies: sequence b, whose first unit is `base`.
 struct Where {
     int64_t total, share;   // units of the call, units of a CTA
@@ -70,7 +76,7 @@ __device__ inline Where find_start(const AttnArgs &a, int64_t cta, int64_t grid,
     const int per = (a.B + threads - 1) / threads;
     const int b0 = min(a.B, t * per), b1 = min(a.B, b0 + per);
     int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += tiles_of(a, b);
+    for (int b = b0; b < b1; ++b) mine += units_of(a, b);
     int64_t inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -89,12 +95,11 @@ __device__ inline Where find_start(const AttnArgs &a, int64_t cta, int64_t grid,
     Where r;
     r.total = total * heads;
     r.share = (r.total + grid - 1) / grid;
-    if (r.share < a.min_share) r.share = a.min_share;
     const int64_t start = cta * r.share;
     int64_t pre = before + inc - mine;
     if (start >= pre * heads && start < (pre + mine) * heads) {
         for (int b = b0; b < b1; ++b) {
-            const int64_t n = tiles_of(a, b);
+            const int64_t n = units_of(a, b);
             if (start < (pre + n) * heads) {
                 scratch[34] = b;
                 scratch[35] = pre * heads;
@@ -143,17 +148,20 @@ __device__ __forceinline__ void for_pieces(const AttnArgs &a, int64_t *scratch, 
     const int64_t end = u + w.share < w.total ? u + w.share : w.total;
     while (u < end) {
         const Seen s = seen_of(a, b);
-        const int n = (s.hi - s.lo + a.tile - 1) / a.tile;
-        if (u - base >= int64_t(n) * heads) {   // past this sequence
-            base += int64_t(n) * heads;
+        const int n = (s.hi - s.lo + a.tile - 1) / a.tile, units = n ? n + a.lead : 0;
+        if (u - base >= int64_t(units) * heads) {   // past this sequence
+            base += int64_t(units) * heads;
             ++b;
             continue;
         }
-        const int hseg = int((u - base) / n), t0 = int((u - base) - int64_t(hseg) * n);
-        const int t1 = int(end - u < n - t0 ? t0 + (end - u) : n);
-        const int lo = s.lo + t0 * a.tile, hi = t1 == n ? s.hi : s.lo + t1 * a.tile;
-        f(b, hseg, lo, hi, t0 == 0 && t1 == n ? -1 : 2 * int(blockIdx.x) + (t0 == 0));
-        u += t1 - t0;
+        const int hseg = int((u - base) / units), at = int((u - base) - int64_t(hseg) * units);
+        const int take = int(end - u < units - at ? end - u : units - at);
+        const int t0 = max(at - a.lead, 0), t1 = max(at + take - a.lead, 0);
+        if (t1 > t0) {
+            const int lo = s.lo + t0 * a.tile, hi = t1 == n ? s.hi : s.lo + t1 * a.tile;
+            f(b, hseg, lo, hi, t0 == 0 && t1 == n ? -1 : 2 * int(blockIdx.x) + (t0 == 0));
+        }
+        u += take;
     }
 }
 
@@ -202,7 +210,7 @@ __device__ __forceinline__ void finish_piece(const AttnArgs &a, int b, int hseg,
 // Host side.  How a call is cut: query heads of a group, units, CTAs (a function of the cache's shape and the device
 // alone, so that the workspace's size does not depend on the call's lengths).
 struct AttnPlan {
-    int32_t HG, HS, tile, grid, threads, stages;
+    int32_t HG, HS, tile, lead, grid, threads, stages;
     size_t smem;
 };
 // bf16 and e4m3 rows: the tensor-core kernel (paged_attn_mma.cu).

@@ -18,6 +18,8 @@
 // scale 2^R so far (o is rescaled when R grows, as it is when the running max does).
 // A weight is rounded to 16 bits for its product with V and the rest rounded again, so it enters as a sum of two 16-bit
 // numbers (within 2^-17 for bf16): with one, its rounding is as large as the output's own and showed in the result.
+#include <limits.h>
+
 #include "paged_attn.cuh"
 
 namespace lsa {
@@ -117,6 +119,7 @@ struct Shape {
     static constexpr int kQPer = E4M3 ? 2 : 1;                          // 16-byte q fragments of a block and head group
     static constexpr bool kQInRegs = KB * NT * kQPer * 4 <= 32;
     static constexpr int kQBytes = KB * NT * kQPer * 512;
+    static constexpr int kLanes = kSwizzle ? 8 : 4;                     // lanes that copy a row, piece by piece
     static constexpr int kRows = kStep * kPitch;                        // bytes of a stage's K (or V) rows
     static constexpr int kTail = 16 + (E4M3 ? kStep * 8 : 0);           // entry mask, scales
     static constexpr int kHeads = 8 * NT;
@@ -153,21 +156,48 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int
         const int steps = (hi - lo + C::kStep - 1) / C::kStep;
         const int n = steps > warp ? (steps - warp + warps - 1) / warps : 0;   // of this warp: warp, warp + warps, ...
 
-        auto locate = [&](int j) {
-            const int t = lo + (warp + j * warps) * C::kStep + lane;
-            return j < n && lane < C::kStep && t < hi ? entry_at(a, row, t) : Entry{-1, 0};
+        // lane r places row r of the warp's steps: entry t, slot s of the sequence's page p
+        int t = lo + warp * C::kStep + lane, p = t / a.cache.page_size, s = t - p * a.cache.page_size;
+        const int hop = warps * C::kStep, hop_p = hop / a.cache.page_size, hop_s = hop - hop_p * a.cache.page_size;
+        if (lane >= C::kStep) t = INT_MAX - (1 << 24);     // (past every end; never reaches it)
+        auto locate = [&]() {                              // of the next step
+            Entry e{-1, 0};
+            if (t < hi) {
+                const int64_t page = row[p];
+                if (page >= 0 && page < a.cache.n_pages) {
+                    e.off = page * a.cache.page_stride + s * a.cache.slot_stride;
+                    e.slot = page * a.cache.page_size + s;
+                } else {
+                    raise_err(a.err, LSA_ERR_INVALID);
+                }
+                t += hop;
+                p += hop_p;
+                s += hop_s;
+                if (s >= a.cache.page_size) {
+                    s -= a.cache.page_size;
+                    ++p;
+                }
+            }
+            return e;
         };
-        auto issue = [&](int j, const Entry &e) {
+        const int lr = lane / C::kLanes, lp = lane % C::kLanes;
+        const uint8_t *ksrc = kbase + lp * 16, *vsrc = vbase + lp * 16;
+        auto issue = [&](int j, int stage, const Entry &e) {
             if (j < n) {
-                const uint32_t st = mine + (j % stages) * stage_bytes;
+                const uint32_t st = mine + stage * stage_bytes;
 #pragma unroll
-                for (int i = 0; i < C::kStep * C::kPieces / 32; ++i) {
-                    const int r = (i * 32 + lane) / C::kPieces, p = (i * 32 + lane) % C::kPieces;
+                for (int k = 0; k < C::kStep * C::kLanes / 32; ++k) {
+                    const int r = lr + 32 / C::kLanes * k;
                     const int64_t off = __shfl_sync(0xffffffffu, e.off, r);
-                    const bool ok = off >= 0 && p < nch;
-                    const int64_t from = ok ? off + p * 16 : 0;
-                    cp_async16(st + piece_at(r, p), kbase + from, ok);
-                    if (!latent) cp_async16(st + v_at + piece_at(r, p), vbase + from, ok);
+                    const bool there = off >= 0;
+                    const int64_t from = there ? off : 0;
+                    const uint32_t to = st + piece_at(r, lp);
+#pragma unroll
+                    for (int i = 0; i < C::kPieces / C::kLanes; ++i) {
+                        const bool ok = there && lp + i * C::kLanes < nch;
+                        cp_async16(to + i * C::kLanes * 16, ksrc + from + i * C::kLanes * 16, ok);
+                        if (!latent) cp_async16(to + v_at + i * C::kLanes * 16, vsrc + from + i * C::kLanes * 16, ok);
+                    }
                 }
                 const uint32_t tail = st + v_at + C::kRows;
                 const uint32_t mask = __ballot_sync(0xffffffffu, e.off >= 0);
@@ -182,10 +212,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int
             cp_commit();
         };
 
-        Entry ahead = locate(0);
+        Entry ahead = locate();
         for (int j = 0; j < stages - 1; ++j) {
-            issue(j, ahead);
-            ahead = locate(j + 1);
+            issue(j, j, ahead);
+            ahead = locate();
         }
 
         // q fragments of the piece's heads: lane (g, c) of block kb and head group nt holds head 8 nt + g, piece 4 kb + c
@@ -261,12 +291,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int
                     for (int e = 0; e < 4; ++e) o[p][t][nt][e] = 0.f;
         }
 
-        for (int j = 0; j < n; ++j) {
+        for (int j = 0, now = 0, next = stages - 1; j < n; ++j) {
             cp_wait(stages - 2);
             __syncwarp();
-            issue(j + stages - 1, ahead);
-            ahead = locate(j + stages);
-            const uint32_t st = mine + (j % stages) * stage_bytes, sv = st + v_at, tail = sv + C::kRows;
+            issue(j + stages - 1, next, ahead);
+            ahead = locate();
+            const uint32_t st = mine + now * stage_bytes, sv = st + v_at, tail = sv + C::kRows;
+            now = now + 1 == stages ? 0 : now + 1;
+            next = next + 1 == stages ? 0 : next + 1;
             uint32_t mask;
             asm volatile("ld.shared.b32 %0, [%1];" : "=r"(mask) : "r"(tail));
 
@@ -504,6 +536,7 @@ struct Run {
         p.stages = stages > 4 ? 4 : stages;
         p.threads = warps * 32;
         p.tile = C::kStep * warps;
+        p.lead = 2;
         p.grid = sm_count() * ctas;
         const size_t ring = size_t(p.stages) * warps * stage, join = size_t(warps) * C::kHeads * (D + 2) * 4;
         p.smem = C::kQBytes + (ring > join ? ring : join);
