@@ -189,65 +189,79 @@ __global__ void __launch_bounds__(kThreads) paged_attn_cc(AttnArgs a, int stages
             if (a.seq_len[b] > a.reach) raise_err(a.err, LSA_ERR_CAPACITY);
 }
 
-// Joins a segment's partials (paged_attn.cuh).  CTA (c, i), c >= 1, acts where the segment that its unit c * share cuts
-// was begun by CTA c - 1, for head i of the group; CTA (c, i) also writes sequences c, c + grid, ... that are empty.
-constexpr int kCombineThreads = 128;
-__global__ void __launch_bounds__(kCombineThreads) paged_attn_combine(AttnArgs a, int grid) {
-    __shared__ int64_t scratch[40];
-    __shared__ float red[8];
+// Joins a segment's partials (paged_attn.cuh): CTA (c, i) those of CTA c's record, for head i of the group.  A group of
+// D / 4 threads adds 16-byte pieces of every kGroups-th partial; its first loads are on their way while the weights are
+// made.
+constexpr int kCombineThreads = 256, kAhead = 4;
+__global__ void __launch_bounds__(kCombineThreads) paged_attn_combine(AttnArgs a) {
+    __shared__ float red[2][kCombineThreads / 32];
+    __shared__ float4 sums[kCombineThreads];
     extern __shared__ float wgt[];   // [grid]
     const int c = blockIdx.x, h = blockIdx.y, D = a.cache.D, HS = a.HS;
     pdl_launch_dependents();
     pdl_wait();
-    for (int b = c; b < a.B; b += grid) {
-        if (tiles_of(a, b) != 0) continue;
-        for (int g = 0; g < a.cache.Hkv * a.HG; ++g) {
-            const int in = (g % a.HG) * HS + h;
-            if (in >= a.G) continue;
-            const int64_t hq = int64_t(b) * a.Hq + (g / a.HG) * a.G + in;
-            for (int d = threadIdx.x; d < D; d += kCombineThreads) store_out(a, hq * D + d, 0.f);
-            if (threadIdx.x == 0 && a.lse) a.lse[hq] = -INFINITY;
-        }
+    const Record rec = a.records[c];
+    const int in = (rec.hseg % a.HG) * HS + h;
+    if (rec.b < 0 || in >= a.G) return;
+    const int P = rec.last - c + 1;
+    auto slot = [&](int p) { return int64_t(p == 0 ? 2 * c + 1 : 2 * (c + p)) * HS + h; };
+    const int lanes = D / 4, groups = kCombineThreads / lanes, lane4 = threadIdx.x % lanes, grp = threadIdx.x / lanes;
+    float4 ahead[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+        const int p = grp + i * groups;
+        if (grp < groups && p < P) ahead[i] = reinterpret_cast<const float4 *>(a.part_o + slot(p) * D)[lane4];
     }
-    const Where w = find_start(a, c, grid, scratch);
-    if (w.b < 0) return;
-    const int64_t n = units_of(a, w.b);
-    const int hseg = int((int64_t(c) * w.share - w.base) / n);
-    const int64_t s0 = w.base + hseg * n;
-    // the CTAs with the segment's first and last entries
-    const int64_t c0 = (s0 + a.lead) / w.share, c1 = (s0 + n - 1) / w.share;
-    if (c != c0 + 1 || c > c1) return;
-    const int in = (hseg % a.HG) * HS + h;
-    if (in >= a.G) return;
-    const int P = int(c1 - c0) + 1;
-    auto slot = [&](int p) { return p == 0 ? 2 * c0 + 1 : 2 * (c0 + p); };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float M = -INFINITY;
-    for (int p = threadIdx.x; p < P; p += kCombineThreads) M = fmaxf(M, a.part_ml[(slot(p) * HS + h) * 2]);
+    for (int p = threadIdx.x; p < P; p += kCombineThreads) M = fmaxf(M, a.part_ml[slot(p) * 2]);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-    if (lane == 0) red[warp] = M;
+    if (lane == 0) red[0][warp] = M;
     __syncthreads();
-    M = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+#pragma unroll
+    for (int w = 0; w < kCombineThreads / 32; ++w) M = fmaxf(M, red[0][w]);
     const float ref = M == -INFINITY ? 0.f : M;
     float L = 0.f;
     for (int p = threadIdx.x; p < P; p += kCombineThreads) {
-        const float f = exp2f(a.part_ml[(slot(p) * HS + h) * 2] - ref);
+        const float f = exp2f(a.part_ml[slot(p) * 2] - ref);
         wgt[p] = f;
-        L = fmaf(f, a.part_ml[(slot(p) * HS + h) * 2 + 1], L);
+        L = fmaf(f, a.part_ml[slot(p) * 2 + 1], L);
     }
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
-    if (lane == 0) red[4 + warp] = L;
+    if (lane == 0) red[1][warp] = L;
     __syncthreads();
-    L = (red[4] + red[5]) + (red[6] + red[7]);
-    const int64_t hq = int64_t(w.b) * a.Hq + (hseg / a.HG) * a.G + in;
-    for (int d = threadIdx.x; d < D; d += kCombineThreads) {
-        float v = 0.f;
-#pragma unroll 8
-        for (int p = 0; p < P; ++p) v = fmaf(wgt[p], a.part_o[(slot(p) * HS + h) * D + d], v);
-        store_out(a, hq * D + d, L == 0.f ? 0.f : v / L);
+    L = 0.f;
+#pragma unroll
+    for (int w = 0; w < kCombineThreads / 32; ++w) L += red[1][w];
+
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float f, const float4 &x) {
+        v.x = fmaf(f, x.x, v.x);
+        v.y = fmaf(f, x.y, v.y);
+        v.z = fmaf(f, x.z, v.z);
+        v.w = fmaf(f, x.w, v.w);
+    };
+    if (grp < groups) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (grp + i * groups < P) add(wgt[grp + i * groups], ahead[i]);
+#pragma unroll 4
+        for (int p = grp + kAhead * groups; p < P; p += groups)
+            add(wgt[p], reinterpret_cast<const float4 *>(a.part_o + slot(p) * D)[lane4]);
+        sums[threadIdx.x] = v;
+    }
+    __syncthreads();
+    const int64_t hq = int64_t(rec.b) * a.Hq + (rec.hseg / a.HG) * a.G + in;
+    if (threadIdx.x < lanes) {
+        for (int i = 1; i < groups; ++i) add(1.f, sums[i * lanes + lane4]);
+        const float r = L == 0.f ? 0.f : 1.f / L;
+        store_out(a, hq * D + 4 * lane4, v.x * r);
+        store_out(a, hq * D + 4 * lane4 + 1, v.y * r);
+        store_out(a, hq * D + 4 * lane4 + 2, v.z * r);
+        store_out(a, hq * D + 4 * lane4 + 3, v.w * r);
     }
     if (threadIdx.x == 0 && a.lse) a.lse[hq] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
@@ -276,7 +290,7 @@ AttnPlan plan_cc(const lsa_page_cache &c, int Hq) {
     const size_t entry = size_t(c.D) * 4 * (c.v == c.k ? 1 : 2);
     p.tile = kMaxTile;
     while (p.tile > 4 && p.tile * entry > 24 * 1024) p.tile /= 2;
-    p.lead = 2;
+    p.lead = 6;
     p.stages = 4;
     p.threads = kThreads;
     p.smem = p.stages * p.tile * entry + (size_t(p.HS) * c.D + size_t(kWarps / nhg) * p.HS * (c.D + 2)) * 4;
@@ -345,7 +359,7 @@ lsa_status check_cache(const lsa_page_cache *c, const char *who) {
 
 lsa_status paged_combine(const AttnArgs &a, int grid, cudaStream_t st) {
     const int heads = a.HS < a.G ? a.HS : a.G;
-    LSA_CUDA(launch_pdl(paged_attn_combine, dim3(grid, heads), dim3(kCombineThreads), size_t(grid) * 4, st, a, grid));
+    LSA_CUDA(launch_pdl(paged_attn_combine, dim3(grid, heads), dim3(kCombineThreads), size_t(grid) * 4, st, a));
     LSA_LAUNCHED("paged_attn_combine");
     return LSA_OK;
 }
@@ -356,7 +370,10 @@ lsa_status paged_combine(const AttnArgs &a, int grid, cudaStream_t st) {
 using namespace lsa;
 using namespace lsa::paged;
 
-static size_t workspace_bytes(const AttnPlan &p, int D) { return size_t(p.grid) * 2 * p.HS * (D + 2) * 4; }
+// partial outputs, their (m, l), and the records (D is a multiple of 16 and HS of 4: each part is 16-byte aligned)
+static size_t workspace_bytes(const AttnPlan &p, int D) {
+    return size_t(p.grid) * 2 * p.HS * (D + 2) * 4 + size_t(p.grid) * sizeof(Record);
+}
 
 static lsa_status check_heads(const lsa_page_cache *cache, int32_t Hq, const char *who) {
     LSA_CHECK_ARG(Hq >= 1 && Hq % cache->Hkv == 0, "%s: Hq=%d is not a positive multiple of Hkv=%d", who, Hq,
@@ -422,6 +439,7 @@ extern "C" lsa_status lsa_paged_attn(const void *Q, lsa_dtype q_dtype, int64_t q
     a.lse = lse;
     a.part_o = static_cast<float *>(workspace);
     a.part_ml = a.part_o + int64_t(p.grid) * 2 * p.HS * cache->D;
+    a.records = reinterpret_cast<Record *>(a.part_ml + int64_t(p.grid) * 2 * p.HS * 2);
     a.err = err;
     a.tile = p.tile;
     a.lead = p.lead;

@@ -2,19 +2,26 @@
 //
 // The work is cut into units.  A segment is one sequence's one group of up to `HS` query heads of a kv head; it has
 // `lead` units for what starting and ending it costs, then one for each `tile` entries.  Units are numbered sequence
-// by sequence, head group by head group, and CTA c of the grid owns the `share` consecutive units from c * share on,
-// so every SM gets the same work whatever the sequences' lengths are (without the leading units a CTA that met many
-// short sequences took twice as long as the others: 198 us against 105 for a ragged batch of 64 sequences of 0 to
-// 16384 entries).  A segment whose entries lie in one CTA's share is finished there; of the others each CTA writes a partial (unnormalised o, and the running max m and sum l of its softmax, both for 2^x), and the combine
-// kernel joins a segment's partials in unit order:
+// by sequence, head group by head group, and CTA c of the grid, which fills the device once, owns the `share`
+// consecutive units from c * share on, so every SM gets the same work whatever the sequences' lengths are (without the
+// leading units a CTA that met many short sequences took twice as long as the others: a batch of 64 sequences of 0 to
+// 16384 entries took 189 us, with two 112, with six 95).  A segment whose entries lie in one CTA's share is finished
+// there; of the others each CTA writes a partial (unnormalised o, and the running max m and sum l of its softmax, both
+// for 2^x), and the combine kernel joins a segment's partials in unit order:
 //     M = max m_c,  L = sum l_c 2^(m_c - M),  o = sum o_c 2^(m_c - M) / L,  lse = (M + log2 L) ln 2.
-// A CTA has at most two partials: slot 2c for the piece that continues a segment, 2c + 1 for one that begins it.
+// A CTA has at most two partials: slot 2c for the piece that continues a segment, 2c + 1 for one that begins it; where
+// it begins one, it records which (a record a CTA), and the record's combine CTAs join it.
 #pragma once
 
 #include "paged.cuh"
 
 namespace lsa {
 namespace paged {
+
+// A segment that CTA c begins and the CTAs up to `last` continue (b < 0: none).
+struct alignas(16) Record {
+    int32_t b, hseg, last, unused;
+};
 
 struct AttnArgs {
     CacheView cache;
@@ -31,6 +38,7 @@ struct AttnArgs {
     void *out;
     float *lse;
     float *part_o, *part_ml;     // [2 * grid][HS][D], [2 * grid][HS][2]
+    Record *records;             // [grid]
     int32_t *err;
     int32_t tile, lead;
     int32_t whole;               // 1: CTA c does segment c and no partials are written
@@ -69,8 +77,8 @@ struct Where {
     int32_t b;              // -1: past the last unit
 };
 
-// Finds the owner of unit `grid index * share` (whole block; `scratch`: 40 int64 of shared memory).
-__device__ inline Where find_start(const AttnArgs &a, int64_t cta, int64_t grid, int64_t *scratch) {
+// Finds where this CTA's first unit lies (whole block; `scratch`: 40 int64 of shared memory).
+__device__ inline Where find_start(const AttnArgs &a, int64_t *scratch) {
     const int threads = blockDim.x, warps = threads >> 5;
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int per = (a.B + threads - 1) / threads;
@@ -94,8 +102,8 @@ __device__ inline Where find_start(const AttnArgs &a, int64_t cta, int64_t grid,
     const int64_t heads = int64_t(a.cache.Hkv) * a.HG;
     Where r;
     r.total = total * heads;
-    r.share = (r.total + grid - 1) / grid;
-    const int64_t start = cta * r.share;
+    r.share = (r.total + gridDim.x - 1) / gridDim.x;
+    const int64_t start = blockIdx.x * r.share;
     int64_t pre = before + inc - mine;
     if (start >= pre * heads && start < (pre + mine) * heads) {
         for (int b = b0; b < b1; ++b) {
@@ -130,6 +138,17 @@ __device__ __forceinline__ Entry entry_at(const AttnArgs &a, const int32_t *row,
     return Entry{page * a.cache.page_stride + s * a.cache.slot_stride, page * a.cache.page_size + s};
 }
 
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void store_out(const AttnArgs &a, int64_t i, float v) {
+    if (a.q_f32) static_cast<float *>(a.out)[i] = v;
+    else static_cast<__nv_bfloat16 *>(a.out)[i] = __float2bfloat16_rn(v);
+}
+
 // The pieces of a CTA, in unit order: f(b, hseg, lo, hi, slot) for entries [lo, hi) of sequence b and segment hseg (kv
 // head hseg / HG, head group hseg % HG); slot: where the piece's partial goes, -1 where the piece is a whole segment.
 template <typename F>
@@ -141,10 +160,19 @@ __device__ __forceinline__ void for_pieces(const AttnArgs &a, int64_t *scratch, 
         f(b, int(blockIdx.x) - b * heads, s.lo, s.hi, -1);
         return;
     }
-    const Where w = find_start(a, blockIdx.x, gridDim.x, scratch);
+    if (threadIdx.x == 0) a.records[blockIdx.x] = Record{-1, 0, 0, 0};
+    // sequences without entries have no units
+    for (int e = blockIdx.x; e < a.B; e += gridDim.x) {
+        if (tiles_of(a, e) != 0) continue;
+        for (int64_t i = threadIdx.x; i < int64_t(a.Hq) * a.cache.D; i += blockDim.x)
+            store_out(a, int64_t(e) * a.Hq * a.cache.D + i, 0.f);
+        if (a.lse)
+            for (int i = threadIdx.x; i < a.Hq; i += blockDim.x) a.lse[int64_t(e) * a.Hq + i] = -INFINITY;
+    }
+    const Where w = find_start(a, scratch);
     if (w.b < 0) return;
     int b = w.b;
-    int64_t base = w.base, u = int64_t(blockIdx.x) * w.share;
+    int64_t base = w.base, u = blockIdx.x * w.share;
     const int64_t end = u + w.share < w.total ? u + w.share : w.total;
     while (u < end) {
         const Seen s = seen_of(a, b);
@@ -159,21 +187,12 @@ __device__ __forceinline__ void for_pieces(const AttnArgs &a, int64_t *scratch, 
         const int t0 = max(at - a.lead, 0), t1 = max(at + take - a.lead, 0);
         if (t1 > t0) {
             const int lo = s.lo + t0 * a.tile, hi = t1 == n ? s.hi : s.lo + t1 * a.tile;
+            if (t0 == 0 && t1 < n && threadIdx.x == 0)
+                a.records[blockIdx.x] = Record{b, hseg, int32_t((u - at + units - 1) / w.share), 0};
             f(b, hseg, lo, hi, t0 == 0 && t1 == n ? -1 : 2 * int(blockIdx.x) + (t0 == 0));
         }
         u += take;
     }
-}
-
-__device__ __forceinline__ float exp2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ void store_out(const AttnArgs &a, int64_t i, float v) {
-    if (a.q_f32) static_cast<float *>(a.out)[i] = v;
-    else static_cast<__nv_bfloat16 *>(a.out)[i] = __float2bfloat16_rn(v);
 }
 
 // Ends a piece (whole block): joins the `n` parts that its warps left in shared memory, o [n][HS][D], ml [n][HS][2],

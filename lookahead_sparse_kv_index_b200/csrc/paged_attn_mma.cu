@@ -8,8 +8,11 @@
 //     128 bf16) through `stages` cp.async stages and never waits for another warp before the end of a piece;
 //   * K is read from shared memory 16 bytes a lane, straight into A fragments: which 8 (16 for e4m3) elements of a head
 //     dim are a fragment's k index is a free choice as long as q's fragment makes the same one;
-//   * V^T needs pairs of entries side by side for one element: a lane reads 16 bytes of four entries' rows and byte
-//     permutes pair them; the entry of each fragment index is chosen (entry_of) so that neither read has bank conflicts;
+//   * V^T needs pairs of entries side by side for one element: bf16 rows are transposed as they are loaded (ldmatrix),
+//     of e4m3 rows a lane reads 16 bytes of four entries and byte permutes pair them; the entry of each fragment index is
+//     chosen (entry_of) so that no read has bank conflicts;
+//   * the running max is a reference that lags: it moves (and o is rescaled) only when a score passes it by 2^8, so most
+//     steps need neither the max over the step's entries nor a shuffle;
 //   * P^T leaves the accumulators with entries along its rows and has to enter with entries along k: one 8 x 8
 //     movmatrix transpose a tile.
 // Types.  bf16 rows are multiplied as they are.  e4m3 rows become f16 (exactly); q becomes f16 times a power of two of
@@ -55,6 +58,12 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
+// Four 8 x 8 tiles of 16-bit elements, each transposed.
+__device__ __forceinline__ void ldmatrix_trans(uint32_t at, uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+                 : "r"(at));
+}
 // Two e4m3 values (low 16 bits; high 16 bits) to two f16.
 __device__ __forceinline__ void e4m3_to_f16(uint32_t x, uint32_t &lo, uint32_t &hi) {
     asm("{\n\t.reg .b16 a, b;\n\t"
@@ -96,13 +105,16 @@ __device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &
     }
 }
 
-// Staged row of fragment index r (0 .. 15).  With rows an odd number of 16-byte pieces apart, or their pieces permuted
-// by the row's low bits, the rows of indices (2j, 2j + 1) lie 4 pieces apart and those of (0, 2, 4, 6), (1, 3, 5, 7)
-// and so on 2 apart: the eight lanes of a 16-byte read phase (two rows x four pieces for K, four rows x two pieces for
-// V) meet eight different bank groups.
+// Staged row of fragment index r (0 .. 15), chosen so that no read of shared memory has bank conflicts while rows are an
+// odd number of 16-byte pieces apart, or have their pieces permuted by the row's low bits.  A K read's phase is eight
+// lanes with the rows of indices (2j, 2j + 1) and four pieces: these rows lie 4 apart.  V^T of bf16 comes by transposing
+// 8 x 8 loads, whose eight rows are any eight neighbours; V of e4m3 by phases of the rows of (0, 2, 4, 6), (1, 3, 5, 7)
+// and so on and two pieces: rows 2 apart.
+template <bool E4M3>
 __device__ __forceinline__ int entry_of(int r) {
     const int j = (r >> 1) & 3, hi = r >> 3;
-    return r & 1 ? 8 + ((2 * j + 4) & 7) + hi : 2 * j + hi;
+    if (E4M3) return r & 1 ? 8 + ((2 * j + 4) & 7) + hi : 2 * j + hi;
+    return 8 * hi + 4 * (r & 1) + j;
 }
 
 // A shape of the kernel.  KB: 64-byte blocks of a row; NT: groups of 8 query heads.
@@ -114,8 +126,8 @@ struct Shape {
     static constexpr int kM = KB <= 2 ? 2 : 1;                          // 16-entry tiles of a step
     static constexpr int kStep = 16 * kM;
     static constexpr int kElems = E4M3 ? 16 : 8;                        // elements of a piece
-    static constexpr int kPass = (kPieces + 7) / 8;                     // 8-piece passes over a V row
-    static constexpr int kTiles = kElems / 2;                           // O^T tiles of a pass
+    static constexpr int kPass = (kPieces + 7) / 8;                     // e4m3: 8-piece passes over a V row
+    static constexpr int kTiles = E4M3 ? 8 * kPass : kPieces / 2;       // O^T tiles of 16 elements
     static constexpr int kQPer = E4M3 ? 2 : 1;                          // 16-byte q fragments of a block and head group
     static constexpr bool kQInRegs = KB * NT * kQPer * 4 <= 32;
     static constexpr int kQBytes = KB * NT * kQPer * 512;
@@ -127,6 +139,7 @@ struct Shape {
 };
 
 constexpr int kMaxWarps = 4;
+constexpr float kLag = 8.f;
 
 template <bool E4M3, int KB, int NT>
 __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int stages) {
@@ -277,18 +290,16 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int
 #pragma unroll
             for (int x = 0; x < 2; ++x) sf[nt][x] = E4M3 ? scale2 / q_scale[nt * 8 + 2 * c + x] : scale2;
 
-        float m[NT][2], l[NT][2], o[C::kPass][C::kTiles][NT][4];
+        float m[NT][2], l[NT][2], o[C::kTiles][NT][4];
         int R = -100;         // weights are held relative to scales of 2^R (e4m3)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = -INFINITY;
             l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
-            for (int p = 0; p < C::kPass; ++p)
+            for (int t = 0; t < C::kTiles; ++t)
 #pragma unroll
-                for (int t = 0; t < C::kTiles; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[p][t][nt][e] = 0.f;
+                for (int e = 0; e < 4; ++e) o[t][nt][e] = 0.f;
         }
 
         for (int j = 0, now = 0, next = stages - 1; j < n; ++j) {
@@ -320,8 +331,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int
                                                : lds16(qf + ((kb * NT + nt) * C::kQPer + x) * 512 + lane * 16);
 #pragma unroll
                 for (int tm = 0; tm < C::kM; ++tm) {
-                    const uint4 k0 = lds16(st + piece_at(tm * 16 + entry_of(g), kb * 4 + c));
-                    const uint4 k1 = lds16(st + piece_at(tm * 16 + entry_of(g + 8), kb * 4 + c));
+                    const uint4 k0 = lds16(st + piece_at(tm * 16 + entry_of<E4M3>(g), kb * 4 + c));
+                    const uint4 k1 = lds16(st + piece_at(tm * 16 + entry_of<E4M3>(g + 8), kb * 4 + c));
                     if constexpr (E4M3) {
                         const uint32_t u0[4] = {k0.x, k0.y, k0.z, k0.w}, u1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
@@ -351,7 +362,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int
             for (int tm = 0; tm < C::kM; ++tm) {
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    const int r = tm * 16 + entry_of(g + 8 * y);
+                    const int r = tm * 16 + entry_of<E4M3>(g + 8 * y);
                     const bool ok = (mask >> r) & 1u;
                     const float ks = E4M3 ? lds_f(tail + 16 + r * 4) : 1.f;
                     vs[tm][y] = E4M3 ? lds_f(tail + 16 + (C::kStep + r) * 4) : 1.f;
@@ -374,45 +385,50 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int
                 e = min(__reduce_max_sync(0xffffffffu, e), 127);
                 grown = e > R ? e - R : 0;
                 R += grown;
-                const float f = __uint_as_float(uint32_t(127 + 13 - R) << 23);   // 2^(13 - R): weights of up to 2^14
+                const float f = __uint_as_float(uint32_t(127 + 5 - R) << 23);   // 2^(5 - R): weights of up to 2^(5 + 8 + 1)
 #pragma unroll
                 for (int tm = 0; tm < C::kM; ++tm) vs[tm][0] *= f, vs[tm][1] *= f;
             }
-            float ref[NT][2], alpha[NT][2];
             bool moved = grown != 0;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    float v = -INFINITY;
+                for (int x = 0; x < 2; ++x)
 #pragma unroll
-                    for (int tm = 0; tm < C::kM; ++tm) v = fmaxf(v, fmaxf(s[tm][nt][x], s[tm][nt][2 + x]));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                    const float mn = fmaxf(m[nt][x], v);
-                    moved |= mn > m[nt][x];
-                    ref[nt][x] = mn == -INFINITY ? 0.f : mn;
-                    alpha[nt][x] = exp2_approx(m[nt][x] - ref[nt][x]);
-                    m[nt][x] = mn;
-                    l[nt][x] *= alpha[nt][x];
-                }
+                    for (int tm = 0; tm < C::kM; ++tm)
+                        moved |= fmaxf(s[tm][nt][x], s[tm][nt][2 + x]) > m[nt][x] + kLag;
             if (__any_sync(0xffffffffu, moved)) {
                 const float f = E4M3 ? __uint_as_float(uint32_t(max(127 - grown, 0)) << 23) : 1.f;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const float f0 = alpha[nt][0] * f, f1 = alpha[nt][1] * f;
+                    float alpha[2];
 #pragma unroll
-                    for (int p = 0; p < C::kPass; ++p)
+                    for (int x = 0; x < 2; ++x) {
+                        float v = m[nt][x];
 #pragma unroll
-                        for (int t = 0; t < C::kTiles; ++t) {
-                            o[p][t][nt][0] *= f0;
-                            o[p][t][nt][1] *= f1;
-                            o[p][t][nt][2] *= f0;
-                            o[p][t][nt][3] *= f1;
-                        }
+                        for (int tm = 0; tm < C::kM; ++tm) v = fmaxf(v, fmaxf(s[tm][nt][x], s[tm][nt][2 + x]));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                        alpha[x] = exp2_approx(m[nt][x] - (v == -INFINITY ? 0.f : v));
+                        m[nt][x] = v;
+                        l[nt][x] *= alpha[x];
+                        alpha[x] *= f;
+                    }
+#pragma unroll
+                    for (int t = 0; t < C::kTiles; ++t) {
+                        o[t][nt][0] *= alpha[0];
+                        o[t][nt][1] *= alpha[1];
+                        o[t][nt][2] *= alpha[0];
+                        o[t][nt][3] *= alpha[1];
+                    }
                 }
             }
+            float ref[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) ref[nt][x] = m[nt][x] == -INFINITY ? 0.f : m[nt][x];
             uint32_t ph[C::kM][NT][2], pl[C::kM][NT][2];
 #pragma unroll
             for (int tm = 0; tm < C::kM; ++tm)
@@ -430,22 +446,22 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int
                         ph[tm][nt][y] = movmatrix(h);
                         pl[tm][nt][y] = movmatrix(r);
                     }
+            if constexpr (E4M3) {
 #pragma unroll
-            for (int p = 0; p < C::kPass; ++p) {
+                for (int p = 0; p < C::kPass; ++p) {
 #pragma unroll
-                for (int tm = 0; tm < C::kM; ++tm) {
-                    uint4 v[4];
+                    for (int tm = 0; tm < C::kM; ++tm) {
+                        uint4 v[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = tm * 16 + entry_of(2 * c + (i & 1) + 8 * (i >> 1));
-                        v[i] = p * 8 + 7 < C::kPieces || p * 8 + g < C::kPieces ? lds16(sv + piece_at(r, p * 8 + g))
-                                                                             : make_uint4(0, 0, 0, 0);
-                    }
-                    const uint32_t v0[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, v1[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
-                    const uint32_t v8[4] = {v[2].x, v[2].y, v[2].z, v[2].w}, v9[4] = {v[3].x, v[3].y, v[3].z, v[3].w};
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = tm * 16 + entry_of<E4M3>(2 * c + (i & 1) + 8 * (i >> 1));
+                            v[i] = p * 8 + 7 < C::kPieces || p * 8 + g < C::kPieces ? lds16(sv + piece_at(r, p * 8 + g))
+                                                                                 : make_uint4(0, 0, 0, 0);
+                        }
+                        const uint32_t v0[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, v1[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
+                        const uint32_t v8[4] = {v[2].x, v[2].y, v[2].z, v[2].w}, v9[4] = {v[3].x, v[3].y, v[3].z, v[3].w};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if constexpr (E4M3) {
+                        for (int i = 0; i < 4; ++i) {
                             // bytes (e, e') of two entries: elements 4i, 4i + 1, then 4i + 2, 4i + 3
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
@@ -455,27 +471,34 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int
                                 e4m3_to_f16(prmt(v8[i], v9[i], sel), a2, a3);
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) {
-                                    float(&d)[4] = o[p][C::kTiles == 8 ? 2 * i + y : i][nt];
+                                    float(&d)[4] = o[p * 8 + 2 * i + y][nt];
                                     mma<true>(d, a0, a1, a2, a3, ph[tm][nt][0], ph[tm][nt][1]);
                                     mma<true>(d, a0, a1, a2, a3, pl[tm][nt][0], pl[tm][nt][1]);
                                 }
                             }
-                        } else {
-                            const uint32_t a0 = prmt(v0[i], v1[i], 0x5410), a1 = prmt(v0[i], v1[i], 0x7632);
-                            const uint32_t a2 = prmt(v8[i], v9[i], 0x5410), a3 = prmt(v8[i], v9[i], 0x7632);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                mma<false>(o[p][i][nt], a0, a1, a2, a3, ph[tm][nt][0], ph[tm][nt][1]);
-                                mma<false>(o[p][i][nt], a0, a1, a2, a3, pl[tm][nt][0], pl[tm][nt][1]);
-                            }
                         }
                     }
                 }
+            } else {
+                // lane l gives the address of matrix l / 8's row l % 8: pieces 2t, 2t + 1 of entries 0 .. 7, then 8 .. 15
+                const int r = entry_of<E4M3>((lane & 7) + 8 * (lane >> 4));
+#pragma unroll
+                for (int tm = 0; tm < C::kM; ++tm)
+#pragma unroll
+                    for (int t = 0; t < C::kTiles; ++t) {
+                        uint32_t a0, a1, a2, a3;
+                        ldmatrix_trans(sv + piece_at(tm * 16 + r, 2 * t + ((lane >> 3) & 1)), a0, a1, a2, a3);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma<false>(o[t][nt], a0, a1, a2, a3, ph[tm][nt][0], ph[tm][nt][1]);
+                            mma<false>(o[t][nt], a0, a1, a2, a3, pl[tm][nt][0], pl[tm][nt][1]);
+                        }
+                    }
             }
         }
         cp_wait(0);
         __syncthreads();      // the parts overlay every warp's stages
-        const float back = E4M3 ? __uint_as_float(uint32_t(127 - 13 + R) << 23) : 1.f;   // 2^(R - 13)
+        const float back = E4M3 ? __uint_as_float(uint32_t(127 - 5 + R) << 23) : 1.f;   // 2^(R - 5)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -489,15 +512,18 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int
                     pml[(warp * C::kHeads + h) * 2] = m[nt][x];
                     pml[(warp * C::kHeads + h) * 2 + 1] = L;
                 }
+                float *part = po + (size_t(warp) * C::kHeads + h) * D;
 #pragma unroll
-                for (int p = 0; p < C::kPass; ++p)
-#pragma unroll
-                    for (int t = 0; t < C::kTiles; ++t) {
-                        const int d = (p * 8 + g) * C::kElems + 2 * t;
+                for (int t = 0; t < C::kTiles; ++t) {
+                    if constexpr (E4M3) {
+                        const int d = (t / 8 * 8 + g) * 16 + 2 * (t % 8);
                         if (d < D)
-                            *reinterpret_cast<float2 *>(po + (size_t(warp) * C::kHeads + h) * D + d) =
-                                make_float2(o[p][t][nt][x] * back, o[p][t][nt][2 + x] * back);
+                            *reinterpret_cast<float2 *>(part + d) = make_float2(o[t][nt][x] * back, o[t][nt][2 + x] * back);
+                    } else {
+                        if (16 * t + g < D) part[16 * t + g] = o[t][nt][x];
+                        if (16 * t + 8 + g < D) part[16 * t + 8 + g] = o[t][nt][2 + x];
                     }
+                }
             }
         __syncthreads();
         finish_piece(a, b, hseg, slot, warps, po, pml);
@@ -536,7 +562,7 @@ struct Run {
         p.stages = stages > 4 ? 4 : stages;
         p.threads = warps * 32;
         p.tile = C::kStep * warps;
-        p.lead = 2;
+        p.lead = 6;
         p.grid = sm_count() * ctas;
         const size_t ring = size_t(p.stages) * warps * stage, join = size_t(warps) * C::kHeads * (D + 2) * 4;
         p.smem = C::kQBytes + (ring > join ? ring : join);

@@ -271,9 +271,11 @@ def sparse_attn(Q, dtype, kv, kv_row_stride, k_off, v_off, rows, B, Hq, D, k, sc
 #
 # These bindings read sizes, strides and types off the tensors, so they check them: a mismatch is a ValueError, and
 # what the library refuses is an LsaError.  They run on the device that holds the tensors, on its current stream
-# unless `stream` is given (a stream of that device).
+# unless `stream` is given (a stream of that device).  A decode step calls them once a layer, where a call's host time
+# is its cost: the checks build no message unless one fails, and the stream's handle is read without a Stream object.
 
 _ELEM = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3}
+_I32, _FP32 = torch.int32, torch.float32
 
 
 def _need(ok, what):
@@ -281,28 +283,47 @@ def _need(ok, what):
         raise ValueError(what)
 
 
-def _i32(t, name, device, shape):
-    _need(t.dtype == torch.int32 and t.device == device and t.is_contiguous() and tuple(t.shape) == tuple(shape),
-          f"{name}: a contiguous int32 tensor {list(shape)} on {device} is needed, not {t.dtype} {list(t.shape)} on "
-          f"{t.device}")
+def _i32(t, name, device, *shape):
+    """The address of a contiguous int32 tensor of `shape` on `device`."""
+    if t.dtype is not _I32 or t.device != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous int32 tensor {list(shape)} on {device} is needed, not {t.dtype} "
+                         f"{list(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
 def _err_word(err, device):
-    _need(err is None or (err.dtype == torch.int32 and err.device == device and err.numel() == 1),
-          "err: one int32 on the call's device is needed")
-    return _ptr(err)
+    if err is None:
+        return None
+    if err.dtype is not _I32 or err.device != device or err.numel() != 1:
+        raise ValueError(f"err: one int32 on {device} is needed")
+    return err.data_ptr()
+
+
+def _room(t, device):
+    """The address and bytes of a workspace."""
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"workspace: a contiguous tensor on {device} is needed")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def _on(device, f, args, where, stream):
     """Calls the library with `device` current and its current stream, or the one given, as the last argument."""
-    _need(device.type == "cuda", f"{where}: tensors on a CUDA device are needed, not on {device}")
-    _need(stream is None or stream.device == device, f"{where}: the stream is not one of {device}")
-    if device.index == torch.cuda.current_device():
-        _check(f(*args, (stream or torch.cuda.current_stream()).cuda_stream), where)
-        return
-    with torch.cuda.device(device):
-        _check(f(*args, (stream or torch.cuda.current_stream()).cuda_stream), where)
+    i = device.index
+    if device.type != "cuda" or i is None:
+        raise ValueError(f"{where}: tensors on a CUDA device are needed, not on {device}")
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(i)
+    elif stream.device == device:
+        handle = stream.cuda_stream
+    else:
+        raise ValueError(f"{where}: the stream is not one of {device}")
+    if torch._C._cuda_getDevice() == i:
+        status = f(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, handle)
+    if status:
+        raise LsaError(status, where)
 
 
 class PageCache:
@@ -314,20 +335,19 @@ class PageCache:
     """
 
     def __init__(self, k, v=None, k_scale=None, v_scale=None):
-        _need(k.dim() == 4 and k.dtype in _ELEM and (k.stride(3) == 1 or k.shape[3] == 1),
+        _need(k.dim() == 4 and k.dtype in _ELEM and k.stride(3) == 1,
               "k: [n_pages, page_size, Hkv, D] of float32, bfloat16 or float8_e4m3fn with unit stride in D is needed")
         _need(v is None or (v.shape == k.shape and v.stride() == k.stride() and v.dtype == k.dtype
                             and v.device == k.device), "v: the shape, strides, type and device of k are needed")
-        self.latent = v is None or v.data_ptr() == k.data_ptr()
         _need(not (v is None and v_scale is not None), "v_scale goes with v")
         for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
-            _need(s is None or (s.dtype == torch.float32 and s.shape == k.shape[:3] and s.is_contiguous()
+            _need(s is None or (s.dtype is _FP32 and s.shape == k.shape[:3] and s.is_contiguous()
                                 and s.device == k.device),
                   f"{name}: a contiguous float32 tensor {list(k.shape[:3])} on {k.device} is needed")
         if v is None:
             v, v_scale = k, k_scale
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.device = k.device
+        self.device, self.dtype = k.device, k.dtype
         self.n_pages, self.page_size, self.Hkv, self.D = k.shape
         self.desc = PageCacheDesc(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ELEM[k.dtype], self.page_size,
                                   self.Hkv, self.D, self.n_pages, k.stride(0), k.stride(1), k.stride(2))
@@ -335,7 +355,8 @@ class PageCache:
 
 
 def paged_attn_workspace_size(cache, B, Hq) -> int:
-    if cache.device.type != "cuda" or cache.device.index == torch.cuda.current_device():
+    """Bytes of paged_attn's workspace on the cache's device (raises on heads that the library does not run)."""
+    if cache.device.type != "cuda" or cache.device.index == torch._C._cuda_getDevice():
         n = _L.lsa_paged_attn_workspace_size(cache._ref, B, Hq)
     else:
         with torch.cuda.device(cache.device):
@@ -344,11 +365,25 @@ def paged_attn_workspace_size(cache, B, Hq) -> int:
     return int(n)
 
 
-def _table_args(table, device):
-    _need(table.dtype == torch.int32 and table.dim() == 2 and table.device == device
-          and (table.stride(1) == 1 or table.shape[1] == 1),
-          f"table: int32 [rows, max_pages] on {device} with unit stride along a row is needed")
-    return table.data_ptr(), max(table.stride(0), table.shape[1]) if table.shape[0] == 1 else table.stride(0)
+def _table(t, device):
+    """Address, row stride and shape of a page table."""
+    if t.dtype is not _I32 or t.device != device or t.dim() != 2:
+        raise ValueError(f"table: int32 [rows, max_pages] on {device} is needed, not {t.dtype} {list(t.shape)} on "
+                         f"{t.device}")
+    (rows, width), (step, unit) = t.shape, t.stride()
+    if unit != 1 and width > 1:
+        raise ValueError("table: unit stride along a row is needed")
+    return t.data_ptr(), step if rows > 1 else width, rows, width
+
+
+def _heads(t, name, T, H, D, dtype, device):
+    """Address and token stride of heads [T, H, D] that lie side by side in a token."""
+    step = t.stride()
+    if (t.shape != (T, H, D) or t.dtype is not dtype or t.device != device or step[2] != 1
+            or (step[1] != D and H > 1)):
+        raise ValueError(f"{name}: [{T}, {H}, {D}] of {dtype} on {device} with heads side by side is needed, not "
+                         f"{t.dtype} {list(t.shape)} with strides {list(step)} on {t.device}")
+    return t.data_ptr(), step[0] if T > 1 else H * D
 
 
 def paged_attn(Q, cache, table, seq_len, out, workspace, lse=None, window=0, scale=None, err=None, stream=None):
@@ -358,22 +393,23 @@ def paged_attn(Q, cache, table, seq_len, out, workspace, lse=None, window=0, sca
     lse float32 [B, Hq] contiguous; workspace: a contiguous tensor of paged_attn_workspace_size bytes.  window: attend
     only the last `window` entries (0: all).  scale None: 1 / sqrt(D).
     """
-    dev = cache.device
-    _need(Q.dim() == 3 and Q.shape[2] == cache.D and Q.dtype in _ELEM and Q.device == dev
-          and (Q.stride(2) == 1 or Q.shape[2] == 1) and (Q.stride(1) == cache.D or Q.shape[1] == 1),
-          f"Q: [B, Hq, {cache.D}] on {dev} with heads side by side is needed")
+    dev, dtype = cache.device, Q.dtype
     B, Hq, D = Q.shape
-    _need(out.shape == Q.shape and out.dtype == Q.dtype and out.device == dev and out.is_contiguous(),
-          "out: contiguous, of Q's shape, type and device, is needed")
-    _need(lse is None or (lse.dtype == torch.float32 and tuple(lse.shape) == (B, Hq) and lse.device == dev
-                          and lse.is_contiguous()), "lse: contiguous float32 [B, Hq] is needed")
-    _need(workspace.device == dev and workspace.is_contiguous(), "workspace: a contiguous tensor on the cache's device")
-    _need(table.dim() == 2 and table.shape[0] == B, f"table: {B} rows are needed")
-    tp, ts = _table_args(table, dev)
+    if dtype not in _ELEM:
+        raise ValueError(f"Q: float32 or bfloat16 is needed, not {dtype}")
+    qp, qs = _heads(Q, "Q", B, Hq, cache.D, dtype, dev)
+    if out.shape != Q.shape or out.dtype is not dtype or out.device != dev or not out.is_contiguous():
+        raise ValueError("out: a contiguous tensor of Q's shape, type and device is needed")
+    if lse is not None and (lse.dtype is not _FP32 or lse.shape != (B, Hq) or lse.device != dev
+                            or not lse.is_contiguous()):
+        raise ValueError(f"lse: a contiguous float32 tensor [{B}, {Hq}] on {dev} is needed")
+    tp, ts, rows, width = _table(table, dev)
+    if rows != B:
+        raise ValueError(f"table: {B} rows are needed, not {rows}")
+    wp, wn = _room(workspace, dev)
     _on(dev, _L.lsa_paged_attn,
-        (Q.data_ptr(), _ELEM[Q.dtype], Q.stride(0) if B > 1 else Hq * D, cache._ref, tp, ts, table.shape[1],
-         _i32(seq_len, "seq_len", dev, (B,)), B, Hq, int(window), float(D ** -0.5 if scale is None else scale),
-         out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        (qp, _ELEM[dtype], qs, cache._ref, tp, ts, width, _i32(seq_len, "seq_len", dev, B), B, Hq, window,
+         D ** -0.5 if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(), wp, wn,
          _err_word(err, dev)), "lsa_paged_attn", stream)
 
 
@@ -383,7 +419,7 @@ ROPE_KINDS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
 def rope_frequencies(rot_dim, base=10000.0, kind="plain", factor=1.0, orig_len=0, beta_fast=32.0, beta_slow=1.0):
     """(frequencies float64 [rot_dim / 2] on the host, mscale) of a plain or scaled rotation (lsa_rope_frequencies)."""
     _need(kind in ROPE_KINDS, f"kind: one of {', '.join(ROPE_KINDS)} is needed, not {kind!r}")
-    freq, m = torch.empty(max(0, rot_dim // 2), dtype=torch.float64), ctypes.c_float()
+    freq, m = torch.empty(max(1, rot_dim // 2), dtype=torch.float64), ctypes.c_float()
     _check(_L.lsa_rope_frequencies(ROPE_KINDS[kind], rot_dim, base, factor, orig_len, beta_fast, beta_slow,
                                    freq.data_ptr(), ctypes.byref(m)), "lsa_rope_frequencies")
     return freq, float(m.value)
@@ -397,16 +433,17 @@ class Rope:
         _need(freq.dtype == torch.float64 and freq.dim() == 1 and freq.is_contiguous(),
               "freq: a contiguous float64 vector is needed")
         _need(mscale > 0, "mscale must be positive")
-        self.freq = freq
+        self.freq, self.device = freq, freq.device if freq.numel() else None
         self.desc = RopeDesc(_ptr(freq), 2 * freq.numel(), int(interleaved), int(inverse), mscale)
         self._ref = ctypes.byref(self.desc)
 
 
-def _heads(t, name, T, H, D, dtype, device):
-    _need(t.dim() == 3 and tuple(t.shape) == (T, H, D) and t.dtype == dtype and t.device == device
-          and (t.stride(2) == 1 or D == 1) and (t.stride(1) == D or H == 1),
-          f"{name}: [{T}, {H}, {D}] of {dtype} on {device} with heads side by side is needed")
-    return t.data_ptr(), t.stride(0) if T > 1 else H * D
+def _weight(w, name, D, dtype, device):
+    if w is None:
+        return None
+    if w.dtype is not dtype or w.shape != (D,) or not w.is_contiguous() or w.device != device:
+        raise ValueError(f"{name}: a contiguous tensor [{D}] of {dtype} on {device} is needed")
+    return w.data_ptr()
 
 
 def qk_norm_rope(q, k=None, v=None, *, q_out, k_out=None, q_weight=None, k_weight=None, eps=1e-6, pos=None, rope=None,
@@ -418,30 +455,32 @@ def qk_norm_rope(q, k=None, v=None, *, q_out, k_out=None, q_weight=None, k_weigh
     k_out likewise, or q and k themselves.  q_weight, k_weight [D]: norm weights, None: no norm.  pos int32 [T] with
     rope.  With cache: token t becomes entry at[t] of table row seq[t] (row t if seq is None).
     """
-    dev = q.device
-    _need(q.dim() == 3 and q.dtype in (torch.float32, torch.bfloat16), "q: [T, Hq, D] of float32 or bfloat16 is needed")
+    dev, dtype = q.device, q.dtype
     T, Hq, D = q.shape
-    Hkv = 0 if k is None else k.shape[1]
-    qp, qs = _heads(q, "q", T, Hq, D, q.dtype, dev)
-    qop, qos = _heads(q_out, "q_out", T, Hq, D, q.dtype, dev)
-    kp, ks = (None, 0) if k is None else _heads(k, "k", T, Hkv, D, q.dtype, dev)
-    kop, kos = (None, 0) if k_out is None else _heads(k_out, "k_out", T, Hkv, D, q.dtype, dev)
-    vp, vs = (None, 0) if v is None else _heads(v, "v", T, Hkv, D, q.dtype, dev)
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        _need(w is None or (w.dtype == q.dtype and tuple(w.shape) == (D,) and w.is_contiguous() and w.device == dev),
-              f"{name}: contiguous [{D}] of {q.dtype} on {dev} is needed")
-    _need(rope is None or rope.freq.device == dev or rope.freq.numel() == 0, "rope: freq on q's device is needed")
-    tp, ts, rows, pages = None, 0, 0, 0
+    if dtype not in _ELEM:
+        raise ValueError(f"q: float32 or bfloat16 is needed, not {dtype}")
+    Hkv, kp, ks, kop, kos, vp, vs, tp, ts, rows, width = 0, None, 0, None, 0, None, 0, None, 0, 0, 0
+    qp, qs = _heads(q, "q", T, Hq, D, dtype, dev)
+    qop, qos = _heads(q_out, "q_out", T, Hq, D, dtype, dev)
+    if k is not None:
+        Hkv = k.shape[1]
+        kp, ks = _heads(k, "k", T, Hkv, D, dtype, dev)
+    if k_out is not None:
+        kop, kos = _heads(k_out, "k_out", T, Hkv, D, dtype, dev)
+    if v is not None:
+        vp, vs = _heads(v, "v", T, Hkv, D, dtype, dev)
+    if rope is not None and rope.device != dev and rope.device is not None:
+        raise ValueError(f"rope: freq on {dev} is needed")
     if cache is not None:
-        _need(cache.device == dev, "cache: on q's device is needed")
-        _need(table is not None and at is not None, "a cache needs table and at")
-        tp, ts = _table_args(table, dev)
-        rows, pages = table.shape
+        if cache.device != dev or table is None or at is None:
+            raise ValueError(f"cache: one on {dev}, with table and at, is needed")
+        tp, ts, rows, width = _table(table, dev)
     _on(dev, _L.lsa_qk_norm_rope,
-        (qp, qs, qop, qos, kp, ks, kop, kos, vp, vs, _ELEM[q.dtype], T, Hq, Hkv, D, _ptr(q_weight), _ptr(k_weight),
-         eps, None if pos is None else _i32(pos, "pos", dev, (T,)), None if rope is None else rope._ref,
-         None if cache is None else cache._ref, tp, ts, rows, pages,
-         None if seq is None else _i32(seq, "seq", dev, (T,)), None if at is None else _i32(at, "at", dev, (T,)),
+        (qp, qs, qop, qos, kp, ks, kop, kos, vp, vs, _ELEM[dtype], T, Hq, Hkv, D,
+         _weight(q_weight, "q_weight", D, dtype, dev), _weight(k_weight, "k_weight", D, dtype, dev), eps,
+         None if pos is None else _i32(pos, "pos", dev, T), None if rope is None else rope._ref,
+         None if cache is None else cache._ref, tp, ts, rows, width,
+         None if seq is None else _i32(seq, "seq", dev, T), None if at is None else _i32(at, "at", dev, T),
          _err_word(err, dev)), "lsa_qk_norm_rope", stream)
 
 
@@ -450,14 +489,14 @@ class PageTable:
     refs int32 [n_pages], contiguous, on one device."""
 
     def __init__(self, table, length, refs, page_size):
-        _need(table.dim() == 2, "table: [n_rows, max_pages] is needed")
+        _need(table.dim() == 2 and refs.dim() == 1, "table: [n_rows, max_pages] and refs: [n_pages] are needed")
         self.table, self.len, self.refs, self.page_size = table, length, refs, int(page_size)
         self.device = table.device
         self.n_rows, self.max_pages = table.shape
         self.n_pages = refs.numel()
-        self.desc = PageTableDesc(_i32(table, "table", self.device, table.shape),
-                                  _i32(length, "length", self.device, (self.n_rows,)),
-                                  _i32(refs, "refs", self.device, (self.n_pages,)), self.n_rows, self.max_pages,
+        self.desc = PageTableDesc(_i32(table, "table", self.device, *table.shape),
+                                  _i32(length, "length", self.device, self.n_rows),
+                                  _i32(refs, "refs", self.device, self.n_pages), self.n_rows, self.max_pages,
                                   self.page_size, self.n_pages)
         self._ref = ctypes.byref(self.desc)
 
@@ -471,23 +510,23 @@ class PageTable:
 
 def page_grow(pages, add, err=None, stream=None):
     """Row r of `pages` becomes add[r] entries longer and takes the pages that needs (lsa_page_grow)."""
-    _on(pages.device, _L.lsa_page_grow, (pages._ref, _i32(add, "add", pages.device, (pages.n_rows,)),
-                                         _err_word(err, pages.device)), "lsa_page_grow", stream)
+    dev = pages.device
+    _on(dev, _L.lsa_page_grow, (pages._ref, _i32(add, "add", dev, pages.n_rows), _err_word(err, dev)),
+        "lsa_page_grow", stream)
 
 
 def page_fork(pages, src, dst, copy_src, copy_dst, err=None, stream=None):
     """Row dst[i] becomes a copy of row src[i]; (copy_src, copy_dst): the pages to copy, -1 for none (lsa_page_fork)."""
     dev, n = pages.device, src.numel()
     _on(dev, _L.lsa_page_fork,
-        (pages._ref, _i32(src, "src", dev, (n,)), _i32(dst, "dst", dev, (n,)), n,
-         _i32(copy_src, "copy_src", dev, (n,)), _i32(copy_dst, "copy_dst", dev, (n,)), _err_word(err, dev)),
-        "lsa_page_fork", stream)
+        (pages._ref, _i32(src, "src", dev, n), _i32(dst, "dst", dev, n), n, _i32(copy_src, "copy_src", dev, n),
+         _i32(copy_dst, "copy_dst", dev, n), _err_word(err, dev)), "lsa_page_fork", stream)
 
 
 def page_free(pages, rows, err=None, stream=None):
     """The rows give back their pages and become empty (lsa_page_free)."""
-    _on(pages.device, _L.lsa_page_free, (pages._ref, _i32(rows, "rows", pages.device, (rows.numel(),)), rows.numel(),
-                                         _err_word(err, pages.device)), "lsa_page_free", stream)
+    dev, n = pages.device, rows.numel()
+    _on(dev, _L.lsa_page_free, (pages._ref, _i32(rows, "rows", dev, n), n, _err_word(err, dev)), "lsa_page_free", stream)
 
 
 def page_compact_workspace_size(n_pages) -> int:
@@ -496,22 +535,20 @@ def page_compact_workspace_size(n_pages) -> int:
 
 def page_compact(pages, table_out, refs_out, move_src, move_dst, n_moves, workspace, stream=None):
     """Packs the held pages to the pool's front (lsa_page_compact); the moves go to page_copy of each layer's cache."""
-    dev = pages.device
-    _need(workspace.device == dev and workspace.is_contiguous(), "workspace: a contiguous tensor on the books' device")
+    dev, n = pages.device, pages.n_pages
+    wp, wn = _room(workspace, dev)
     _on(dev, _L.lsa_page_compact,
-        (pages._ref, _i32(table_out, "table_out", dev, pages.table.shape), _i32(refs_out, "refs_out", dev,
-                                                                               (pages.n_pages,)),
-         _i32(move_src, "move_src", dev, (pages.n_pages,)), _i32(move_dst, "move_dst", dev, (pages.n_pages,)),
-         _i32(n_moves, "n_moves", dev, (1,)), workspace.data_ptr(), workspace.numel() * workspace.element_size()),
-        "lsa_page_compact", stream)
+        (pages._ref, _i32(table_out, "table_out", dev, pages.n_rows, pages.max_pages),
+         _i32(refs_out, "refs_out", dev, n), _i32(move_src, "move_src", dev, n), _i32(move_dst, "move_dst", dev, n),
+         _i32(n_moves, "n_moves", dev, 1), wp, wn), "lsa_page_compact", stream)
 
 
 def page_copy(cache, src, dst, count=None, err=None, stream=None):
     """Copies pages src[i] -> dst[i] of a PageCache (lsa_page_copy), the first `count` of them where that is given."""
     dev, n = cache.device, src.numel()
     _on(dev, _L.lsa_page_copy,
-        (cache._ref, _i32(src, "src", dev, (n,)), _i32(dst, "dst", dev, (n,)), n,
-         None if count is None else _i32(count, "count", dev, (1,)), _err_word(err, dev)), "lsa_page_copy", stream)
+        (cache._ref, _i32(src, "src", dev, n), _i32(dst, "dst", dev, n), n,
+         None if count is None else _i32(count, "count", dev, 1), _err_word(err, dev)), "lsa_page_copy", stream)
 
 
 # ----------------------------------------------------------- decode context
