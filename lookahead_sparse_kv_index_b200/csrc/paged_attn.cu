@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kThreads) paged_attn_cc(AttnArgs a, int stages
 
     pdl_launch_dependents();
     pdl_wait();
-    for_pieces(a, scratch, [&](int b, int hseg, int lo, int hi, int slot) {
+    for_pieces(a, blockIdx.x, gridDim.x, scratch, [&](int b, int hseg, int lo, int hi, int slot) {
         const int kvh = hseg / a.HG, first = (hseg % a.HG) * HS;
         const int32_t *row = a.table + int64_t(b) * a.table_stride;
         const int ntiles = (hi - lo + tile - 1) / tile;
@@ -319,7 +319,10 @@ lsa_status dispatch_cc(const AttnArgs &a, const AttnPlan &p, int grid, cudaStrea
     }
 }
 
-AttnPlan plan_of(const lsa_page_cache &c, int Hq) { return c.dtype == LSA_F32 ? plan_cc(c, Hq) : plan_mma(c, Hq); }
+AttnPlan plan_of(const lsa_page_cache &c, int Hq) {
+    if (c.dtype == LSA_F32) return plan_cc(c, Hq);
+    return latent_supported(c, Hq) ? plan_latent(c, Hq) : plan_mma(c, Hq);
+}
 
 // A segment of so few units is done by one CTA, without partials and a second launch.
 constexpr int kWholeUnits = 8;
@@ -370,7 +373,7 @@ lsa_status paged_combine(const AttnArgs &a, int grid, cudaStream_t st) {
 using namespace lsa;
 using namespace lsa::paged;
 
-// partial outputs, their (m, l), and the records (D is a multiple of 16 and HS of 4: each part is 16-byte aligned)
+// partial outputs, their (m, l), and the records (D is a multiple of 16: every part is 16-byte aligned)
 static size_t workspace_bytes(const AttnPlan &p, int D) {
     return size_t(p.grid) * 2 * p.HS * (D + 2) * 4 + size_t(p.grid) * sizeof(Record);
 }
@@ -449,7 +452,8 @@ extern "C" lsa_status lsa_paged_attn(const void *Q, lsa_dtype q_dtype, int64_t q
     a.whole = most <= int64_t(kWholeUnits) * p.tile && segments < (int64_t(1) << 31);
     const int grid = a.whole ? int(segments) : p.grid;
     cudaStream_t st = as_stream(stream);
-    s = cache->dtype == LSA_F32 ? dispatch_cc(a, p, grid, st) : launch_mma(*cache, a, p, grid, st);
+    s = cache->dtype == LSA_F32 ? dispatch_cc(a, p, grid, st)
+        : latent_supported(*cache, Hq) ? launch_latent(*cache, a, grid, st) : launch_mma(*cache, a, p, grid, st);
     if (s != LSA_OK || a.whole) return s;
     return paged_combine(a, grid, st);
 }

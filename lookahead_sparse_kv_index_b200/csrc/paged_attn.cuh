@@ -77,8 +77,8 @@ struct Where {
     int32_t b;              // -1: past the last unit
 };
 
-// Finds where this CTA's first unit lies (whole block; `scratch`: 40 int64 of shared memory).
-__device__ inline Where find_start(const AttnArgs &a, int64_t *scratch) {
+// Finds where the first unit of CTA `cta` of `ctas` lies (whole block; `scratch`: 40 int64 of shared memory).
+__device__ inline Where find_start(const AttnArgs &a, int64_t cta, int64_t ctas, int64_t *scratch) {
     const int threads = blockDim.x, warps = threads >> 5;
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int per = (a.B + threads - 1) / threads;
@@ -102,8 +102,8 @@ __device__ inline Where find_start(const AttnArgs &a, int64_t *scratch) {
     const int64_t heads = int64_t(a.cache.Hkv) * a.HG;
     Where r;
     r.total = total * heads;
-    r.share = (r.total + gridDim.x - 1) / gridDim.x;
-    const int64_t start = blockIdx.x * r.share;
+    r.share = (r.total + ctas - 1) / ctas;
+    const int64_t start = cta * r.share;
     int64_t pre = before + inc - mine;
     if (start >= pre * heads && start < (pre + mine) * heads) {
         for (int b = b0; b < b1; ++b) {
@@ -149,30 +149,30 @@ __device__ __forceinline__ void store_out(const AttnArgs &a, int64_t i, float v)
     else static_cast<__nv_bfloat16 *>(a.out)[i] = __float2bfloat16_rn(v);
 }
 
-// The pieces of a CTA, in unit order: f(b, hseg, lo, hi, slot) for entries [lo, hi) of sequence b and segment hseg (kv
+// The pieces of CTA `cta` of `ctas` (a cluster counts as one), in unit order: f(b, hseg, lo, hi, slot) for entries [lo, hi) of sequence b and segment hseg (kv
 // head hseg / HG, head group hseg % HG); slot: where the piece's partial goes, -1 where the piece is a whole segment.
 template <typename F>
-__device__ __forceinline__ void for_pieces(const AttnArgs &a, int64_t *scratch, F f) {
+__device__ __forceinline__ void for_pieces(const AttnArgs &a, int cta, int ctas, int64_t *scratch, F f) {
     const int heads = a.cache.Hkv * a.HG;
     if (a.whole) {
-        const int b = blockIdx.x / heads;
+        const int b = cta / heads;
         const Seen s = seen_of(a, b);
-        f(b, int(blockIdx.x) - b * heads, s.lo, s.hi, -1);
+        f(b, cta - b * heads, s.lo, s.hi, -1);
         return;
     }
-    if (threadIdx.x == 0) a.records[blockIdx.x] = Record{-1, 0, 0, 0};
+    if (threadIdx.x == 0) a.records[cta] = Record{-1, 0, 0, 0};
     // sequences without entries have no units
-    for (int e = blockIdx.x; e < a.B; e += gridDim.x) {
+    for (int e = cta; e < a.B; e += ctas) {
         if (tiles_of(a, e) != 0) continue;
         for (int64_t i = threadIdx.x; i < int64_t(a.Hq) * a.cache.D; i += blockDim.x)
             store_out(a, int64_t(e) * a.Hq * a.cache.D + i, 0.f);
         if (a.lse)
             for (int i = threadIdx.x; i < a.Hq; i += blockDim.x) a.lse[int64_t(e) * a.Hq + i] = -INFINITY;
     }
-    const Where w = find_start(a, scratch);
+    const Where w = find_start(a, cta, ctas, scratch);
     if (w.b < 0) return;
     int b = w.b;
-    int64_t base = w.base, u = blockIdx.x * w.share;
+    int64_t base = w.base, u = cta * w.share;
     const int64_t end = u + w.share < w.total ? u + w.share : w.total;
     while (u < end) {
         const Seen s = seen_of(a, b);
@@ -188,8 +188,8 @@ __device__ __forceinline__ void for_pieces(const AttnArgs &a, int64_t *scratch, 
         if (t1 > t0) {
             const int lo = s.lo + t0 * a.tile, hi = t1 == n ? s.hi : s.lo + t1 * a.tile;
             if (t0 == 0 && t1 < n && threadIdx.x == 0)
-                a.records[blockIdx.x] = Record{b, hseg, int32_t((u - at + units - 1) / w.share), 0};
-            f(b, hseg, lo, hi, t0 == 0 && t1 == n ? -1 : 2 * int(blockIdx.x) + (t0 == 0));
+                a.records[cta] = Record{b, hseg, int32_t((u - at + units - 1) / w.share), 0};
+            f(b, hseg, lo, hi, t0 == 0 && t1 == n ? -1 : 2 * cta + (t0 == 0));
         }
         u += take;
     }
@@ -235,6 +235,10 @@ struct AttnPlan {
 // bf16 and e4m3 rows: the tensor-core kernel (paged_attn_mma.cu).
 AttnPlan plan_mma(const lsa_page_cache &c, int Hq);
 lsa_status launch_mma(const lsa_page_cache &c, const AttnArgs &a, const AttnPlan &p, int grid, cudaStream_t st);
+// A latent bf16 head of 512 under more than 8 query heads: the tcgen05 kernel (paged_attn_latent.cu).
+bool latent_supported(const lsa_page_cache &c, int Hq);
+AttnPlan plan_latent(const lsa_page_cache &c, int Hq);
+lsa_status launch_latent(const lsa_page_cache &c, const AttnArgs &a, int grid, cudaStream_t st);
 lsa_status paged_combine(const AttnArgs &a, int grid, cudaStream_t st);
 
 }  // namespace paged

@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int
         finish_piece(a, b, hseg, slot, warps, po, pml);
         __syncthreads();
     };
-    for_pieces(a, scratch, do_piece);
+    for_pieces(a, blockIdx.x, gridDim.x, scratch, do_piece);
     if (blockIdx.x == 0 && a.err)
         for (int b = threadIdx.x; b < a.B; b += blockDim.x)
             if (a.seq_len[b] > a.reach) raise_err(a.err, LSA_ERR_CAPACITY);
