@@ -453,7 +453,7 @@ extern "C" lsa_status lsa_paged_attn(const void *Q, lsa_dtype q_dtype, int64_t q
     const int grid = a.whole ? int(segments) : p.grid;
     cudaStream_t st = as_stream(stream);
     s = cache->dtype == LSA_F32 ? dispatch_cc(a, p, grid, st)
-        : latent_supported(*cache, Hq) ? launch_latent(*cache, a, grid, st) : launch_mma(*cache, a, p, grid, st);
+        : latent_supported(*cache, Hq) ? launch_latent(a, grid, st) : launch_mma(*cache, a, p, grid, st);
     if (s != LSA_OK || a.whole) return s;
     return paged_combine(a, grid, st);
 }

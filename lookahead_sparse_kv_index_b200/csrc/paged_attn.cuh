@@ -238,7 +238,7 @@ lsa_status launch_mma(const lsa_page_cache &c, const AttnArgs &a, const AttnPlan
 // A latent bf16 head of 512 under more than 8 query heads: the tcgen05 kernel (paged_attn_latent.cu).
 bool latent_supported(const lsa_page_cache &c, int Hq);
 AttnPlan plan_latent(const lsa_page_cache &c, int Hq);
-lsa_status launch_latent(const lsa_page_cache &c, const AttnArgs &a, int grid, cudaStream_t st);
+lsa_status launch_latent(const AttnArgs &a, int grid, cudaStream_t st);
 lsa_status paged_combine(const AttnArgs &a, int grid, cudaStream_t st);
 
 }  // namespace paged

@@ -2,21 +2,24 @@
 // tcgen05 (paged_attn.cuh says how the work is cut).
 //
 // 128 query heads on one row make 256 flops a byte: tensor and HBM time are about equal, so both have to run all the
-// time.  O for 128 heads x 512 elements fills the tensor memory, and Q with two tiles of rows does not fit in shared
-// memory, so two CTAs (a cluster) share a piece and split the 512 columns:
-//   * CTA r holds Q's and the rows' columns 256 r .. 256 r + 255: it multiplies S_r = Q_r K_r^T (M = 128 heads, N = 64
-//     entries, K = 256) and, from the same staged rows read MN-major, O_r += P V_r (N = 256, K = 64).  No row is read
-//     twice and no product is made twice;
-//   * S = S_0 + S_1: each CTA writes its S_r to the other's shared memory (32 KB a tile) and adds what it gets, so both
-//     hold the same scores and make the same weights;
+// time.  O for 128 heads x 512 elements would fill the tensor memory, so two CTAs (a cluster) share a piece and split the
+// 512 columns:
+//   * CTA r holds the rows' columns 256 r .. 256 r + 255: it multiplies S_r = Q_r K_r^T (M = 128 heads, N = 64 entries,
+//     K = 256) and, from the same staged rows read MN-major, O_r += P V_r (N = 256, K = 64).  No row is read twice and
+//     no product is made twice;
+//   * S = S_0 + S_1: each CTA stores its S_r into the other's shared memory (32 KB a tile, st.async, which counts its
+//     bytes on the other's barrier) and adds what it gets, so both hold the same scores and make the same weights;
 //   * P enters as two bf16 numbers (a weight and what its rounding left), as in paged_attn_mma.cu.
-// Eleven warps: 0-7 softmax (thread = head, half of the tile's entries), 8 issues the MMAs, 9-10 copy rows (cp.async,
-// 64 rows x 512 B a tile, three tiles in the ring).  S of tile i + 1 is issued before P V of tile i, so the softmax of a
-// tile runs beside P V of the one before and S of the one after; S has two buffers in tensor memory (columns 256 .. 383),
-// O has columns 0 .. 255.  The running max is a reference that moves, and O is rescaled, only when a score passes it by
-// 2^8.  Every wait is bounded; the two CTAs leave together.
-#include <cuda.h>
-
+// Tensor memory: O in columns 0 .. 255, two buffers of S in 256 .. 383, Q_r (bf16, the MMA's A operand) in 384 .. 511;
+// Q there leaves shared memory to four tiles of rows (32 KB each), P (2 x 16 KB) and two buffers of the other's S.
+// Twelve warps: 0-7 softmax (thread = head, half of the tile's entries), 8 issues the MMAs, 9-10 copy rows (cp.async),
+// 11 tells the other CTA what was read of its scores (a release that would hold the softmax up for 350 cycles a tile).
+// A tile passes load, S, exchange, softmax, P V; what counts is that these overlap.  S of tile i + 2 is issued as soon as
+// the scores of tile i are in registers, before P V of tile i, and the softmax warps send their S of tile i + 1 before
+// they take up what came for tile i, so neither the exchange nor a product is waited for (with S of tile i + 1 issued
+// after P V of tile i - 1 the softmax and the tensor pipe took turns: 423 us for 128 heads over 4 x 131072 entries).  The
+// running max is a reference that moves, and O is rescaled, only when a score passes it by 2^8; a barrier that every
+// tile needs anyway tells whether one did.  Every wait is bounded; the two CTAs leave together.
 #include "paged_attn.cuh"
 #include "tc_ptx.cuh"
 
@@ -26,24 +29,24 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kHeads = 128, kD = 512, kCols = 256, kTile = 64, kStages = 3;
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kLoadWarps = 2;
-constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
+constexpr int kHeads = 128, kD = 512, kCols = 256, kTile = 64, kStages = 4;
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kLoadWarps = 2, kAckWarp = 11;
+constexpr int kThreads = 32 * (kAckWarp + 1);
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
-constexpr int kQSlice = kHeads * 128;            // 64 columns of Q: 16 KB
-constexpr int kQBytes = 4 * kQSlice;
+constexpr int kTmemS = kCols, kTmemQ = kCols + 2 * kTile;
 constexpr int kBlock = kTile * 128;              // 64 columns of a tile: 8 KB
 constexpr int kStageBytes = 4 * kBlock;
 constexpr int kPBytes = kHeads * 128;            // weights of a tile: 16 KB (and as much for what their rounding left)
 constexpr int kRecvBytes = kHeads * kTile * 4;   // the other CTA's S of a tile
-constexpr size_t kSmem = 1024 + kQBytes + kStages * size_t(kStageBytes) + 2 * kPBytes + kRecvBytes;
+constexpr size_t kSmem = 1024 + kStages * size_t(kStageBytes) + 2 * kPBytes + 2 * kRecvBytes;
 // the S buffer is not reused: the other CTA may already send the next piece's
-static_assert(kSoftWarps * 32 * 32 * 4 <= 2 * kPBytes, "a warp's 32 x 32 output block is staged over the weights");
+static_assert(kSoftWarps * 32 * 32 * 4 <= 2 * kPBytes, "a warp stages 32 x 32 outputs over the weights");
 static_assert(kLoadWarps * 32 == kTile, "a load warp's lanes place one row each");
 constexpr float kLag = 8.f;
 
 struct Bars {
-    uint64_t q_full, kv_full[kStages], kv_free[kStages], mask_full[kStages], s_full[2], p_full, s_recv, send_ok, drain;
+    uint64_t q_full, kv_full[kStages], kv_free[kStages], mask_full[kStages], s_full[2], s_free[2], s_recv[2], send_ok[2], p_full,
+        drain;
 };
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, uint32_t src_bytes) {
@@ -74,30 +77,45 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w)
+// Stores 16 bytes in the other CTA and counts them on a barrier of its.
+__device__ __forceinline__ void st_async(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::
+                     "r"(addr), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
                  : "memory");
 }
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+// D[tmem] (+)= A[tmem] * B[smem]^T, bf16 inputs, f32 accumulate.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// mbar_wait whose success also acquires what the cluster's other CTA released.
+// mbar_try_wait and mbar_wait that also acquire what the cluster's other CTA released.
+__device__ __forceinline__ bool try_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
 __device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    if (try_cluster(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
     while (true) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}\n"
-            : "=r"(done)
-            : "r"(smem_u32(bar)), "r"(parity)
-            : "memory");
-        if (done) return true;
+        if (try_cluster(bar, parity)) return true;
         if (*abort) return false;
         if (global_timer_ns() - t0 > kWaitLimitNs) {
             *abort = 1;
@@ -114,19 +132,11 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::
-            "r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
-        : "memory");
-}
-
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-paged_attn_latent(const __grid_constant__ CUtensorMap qmap, AttnArgs a) {
+paged_attn_latent(AttnArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *qs = smem, *kvs = qs + kQBytes, *ps = kvs + kStages * kStageBytes, *recv = ps + 2 * kPBytes;
+    uint8_t *kvs = smem, *ps = kvs + kStages * kStageBytes, *recv = ps + 2 * kPBytes;
     __shared__ Bars bars;
     __shared__ int64_t scratch[40];
     __shared__ uint32_t tmem_slot;
@@ -142,17 +152,19 @@ paged_attn_latent(const __grid_constant__ CUtensorMap qmap, AttnArgs a) {
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
         abort_flag = 0;
-        mbar_init(&bars.q_full, 1);
+        mbar_init(&bars.q_full, kSoftWarps);
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&bars.kv_full[s], 32 * kLoadWarps);
             mbar_init(&bars.kv_free[s], 1);
             mbar_init(&bars.mask_full[s], kLoadWarps);
         }
-        mbar_init(&bars.s_full[0], 1);
-        mbar_init(&bars.s_full[1], 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bars.s_full[s], 1);
+            mbar_init(&bars.s_recv[s], 1);
+            mbar_init(&bars.s_free[s], kSoftWarps);
+            mbar_init(&bars.send_ok[s], 1);
+        }
         mbar_init(&bars.p_full, kSoftWarps);
-        mbar_init(&bars.s_recv, kSoftWarps);
-        mbar_init(&bars.send_ok, kSoftWarps);
         mbar_init(&bars.drain, 1);
         fence_mbar_init();
     }
@@ -173,7 +185,17 @@ paged_attn_latent(const __grid_constant__ CUtensorMap qmap, AttnArgs a) {
         if (gave_up) return;
         const int kvh = hseg / a.HG, first = (hseg % a.HG) * kHeads;
         const int n = (hi - lo + kTile - 1) / kTile;
-        if (warp >= kLoadWarp) {
+        if (warp == kAckWarp) {
+            // ---- the scores of tile j have been read: the other CTA may send tile j + 2
+            if (lane == 0) {
+                const uint32_t peer_ok = in_cta(smem_u32(&bars.send_ok[0]), peer);
+                for (int j = 0; j < n; ++j) {
+                    const uint32_t g = tiles + j, x = g & 1;
+                    if (!mbar_wait(&bars.s_free[x], (g >> 1) & 1, abort_v, kWaitLimitNs)) break;
+                    arrive_cluster(peer_ok + x * 8);
+                }
+            }
+        } else if (warp >= kLoadWarp) {
             // ---- rows: lane l of warp w places row 32 w + l; the warp then copies its 32 rows, one a pass
             const int w = warp - kLoadWarp;
             const int32_t *row = a.table + int64_t(b) * a.table_stride;
@@ -209,26 +231,24 @@ paged_attn_latent(const __grid_constant__ CUtensorMap qmap, AttnArgs a) {
             if (lane == 0 && n > 0) {
                 constexpr uint32_t kIdescS = idesc_bf16(kHeads, kTile);
                 constexpr uint32_t kIdescO = idesc_bf16(kHeads, kCols) | (1u << 16);   // B (V) is MN-major
-                mbar_arrive_expect_tx(&bars.q_full, kQBytes);
-                for (int i = 0; i < 4; ++i)
-                    tma_load_3d(qs + i * kQSlice, &qmap, &bars.q_full, int(rank) * kCols + i * 64, kvh * a.G + first, b);
                 bool ok = mbar_wait(&bars.q_full, pieces & 1, abort_v, kWaitLimitNs);
                 auto s_tile = [&](int j) {
                     const uint32_t g = tiles + j, s = g % kStages;
                     if (!mbar_wait(&bars.kv_full[s], (g / kStages) & 1, abort_v, kWaitLimitNs)) return false;
+                    if (g >= 2 && !mbar_wait(&bars.s_free[g & 1], ((g >> 1) - 1) & 1, abort_v, kWaitLimitNs)) return false;
                     fence_proxy_async_smem();    // the rows were written by cp.async
                     tc_fence_after();
-                    const uint32_t q = smem_u32(qs), kv = smem_u32(kvs) + s * kStageBytes;
+                    const uint32_t kv = smem_u32(kvs) + s * kStageBytes;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        mma_f16(tmem + kCols + (g & 1) * kTile, desc_sw128(q + (i >> 2) * kQSlice + (i & 3) * 32),
-                                desc_sw128(kv + (i >> 2) * kBlock + (i & 3) * 32), kIdescS, i != 0);
+                    for (int i = 0; i < 16; ++i)      // 16 elements of K: 8 columns of Q
+                        mma_f16_ts(tmem + kTmemS + (g & 1) * kTile, tmem + kTmemQ + i * 8,
+                                   desc_sw128(kv + (i >> 2) * kBlock + (i & 3) * 32), kIdescS, i != 0);
                     mma_commit(&bars.s_full[g & 1]);
                     return true;
                 };
-                ok = ok && s_tile(0);
+                ok = ok && s_tile(0) && (n < 2 || s_tile(1));
                 for (int j = 0; j < n && ok; ++j) {
-                    if (j + 1 < n) ok = s_tile(j + 1);
+                    if (j + 2 < n) ok = s_tile(j + 2);
                     const uint32_t g = tiles + j, s = g % kStages;
                     ok = ok && mbar_wait(&bars.p_full, g & 1, abort_v, kWaitLimitNs);
                     if (!ok) break;
@@ -254,71 +274,117 @@ paged_attn_latent(const __grid_constant__ CUtensorMap qmap, AttnArgs a) {
             const int quarter = warp & 3, half = warp >> 2, head = 32 * quarter + lane;
             const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
             const float scale2 = a.scale * kLog2e;
-            const uint32_t slot_at = smem_u32(recv) + (half * 8 * kHeads + head) * 16;
-            const uint32_t peer_slot = in_cta(slot_at, peer);
-            const uint32_t peer_recv = in_cta(smem_u32(&bars.s_recv), peer), peer_ok = in_cta(smem_u32(&bars.send_ok), peer);
+            const uint32_t slot_at = smem_u32(recv) + (half * 8 * kHeads + head) * 16;   // of 8 pieces, kHeads * 16 apart
+            const uint32_t peer_slot = in_cta(slot_at, peer), peer_recv = in_cta(smem_u32(&bars.s_recv[0]), peer);
             float m = -INFINITY, l = 0.f;
             bool ok = true;
-            for (int j = 0; j < n; ++j) {
-                const uint32_t g = tiles + j, s = g % kStages;
-                ok = mbar_wait(&bars.s_full[g & 1], (g >> 1) & 1, abort_v, kWaitLimitNs);
-                ok = ok && (g == 0 || wait_cluster(&bars.send_ok, (g - 1) & 1, abort_v));
-                if (!named_barrier_and(1, 32 * kSoftWarps, ok)) {
-                    ok = false;
-                    break;
-                }
+            // S_r of tile j to the other CTA
+            auto send = [&](int j) {
+                const uint32_t g = tiles + j, x = g & 1;
+                if (threadIdx.x == 0) mbar_arrive_expect_tx(&bars.s_recv[x], kRecvBytes);   // for what comes here
+                bool sent = mbar_wait(&bars.s_full[x], (g >> 1) & 1, abort_v, kWaitLimitNs);
+                // the other CTA has read tile g - 2, which lay there
+                if (g >= 2) sent = wait_cluster(&bars.send_ok[x], ((g >> 1) - 1) & 1, abort_v) && sent;
+                sent = __all_sync(0xffffffffu, sent);
+                if (!sent) return false;
                 tc_fence_after();
-                uint32_t sv[32];
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    tmem_ld_32x32b_x16(lanes + kCols + (g & 1) * kTile + half * 32 + c * 16,
-                                       *reinterpret_cast<uint32_t(*)[16]>(&sv[c * 16]));
-                tmem_ld_wait();
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t sv[16];
+                    tmem_ld_32x32b_x16(lanes + kTmemS + x * kTile + half * 32 + c * 16, sv);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        st_async(peer_slot + x * kRecvBytes + (4 * c + y) * kHeads * 16, sv[4 * y], sv[4 * y + 1],
+                                 sv[4 * y + 2], sv[4 * y + 3], peer_recv + x * 8);
+                }
+                return true;
+            };
+            if (n > 0) {
+                // Q_r: this thread's head, 128 of the 256 columns, two to a column of tensor memory
+                const int heads = min(kHeads, a.G - first);
+                const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.q) + int64_t(b) * a.q_stride +
+                                                                 (int64_t(kvh) * a.G + first + head) * (kD * 2) +
+                                                                 rank * (kCols * 2) + half * 256);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const uint4 x = head < heads ? q[4 * c + y] : make_uint4(0, 0, 0, 0);
+                        w[4 * y] = x.x;
+                        w[4 * y + 1] = x.y;
+                        w[4 * y + 2] = x.z;
+                        w[4 * y + 3] = x.w;
+                    }
+                    tmem_st_32x32b_x16(lanes + kTmemQ + half * 64 + c * 16, w);
+                }
+                tmem_st_wait();
                 tc_fence_before();
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    st_cluster(peer_slot + c * kHeads * 16, sv[4 * c], sv[4 * c + 1], sv[4 * c + 2], sv[4 * c + 3]);
-                fence_cluster();
                 __syncwarp();
-                if (lane == 0) arrive_cluster(peer_recv);
-                ok = wait_cluster(&bars.s_recv, g & 1, abort_v) &&
-                     mbar_wait(&bars.mask_full[s], (g / kStages) & 1, abort_v, kWaitLimitNs);
-                const uint32_t mask = s_mask[s][half];
+                if (lane == 0) mbar_arrive(&bars.q_full);
+                ok = send(0);
+            }
+            for (int j = 0; j < n; ++j) {
+                const uint32_t g = tiles + j, s = g % kStages, x = g & 1;
+                if (j + 1 < n) ok = send(j + 1) && ok;
+                // three waits, tried together (each takes a hundred cycles even when there is nothing to wait for): the
+                // other CTA's scores, which rows are there, and P V of the tile before, which is done with the weights'
+                // buffer and with O
+                uint64_t *before = &bars.kv_free[(g + kStages - 1) % kStages];
+                const uint32_t before_phase = ((g - 1) / kStages) & 1;
+                const bool t0 = try_cluster(&bars.s_recv[x], (g >> 1) & 1);
+                const bool t1 = mbar_try_wait(&bars.mask_full[s], (g / kStages) & 1);
+                const bool t2 = j == 0 || mbar_try_wait(before, before_phase);
+                ok = ok && (t0 || wait_cluster(&bars.s_recv[x], (g >> 1) & 1, abort_v)) &&
+                     (t1 || mbar_wait(&bars.mask_full[s], (g / kStages) & 1, abort_v, kWaitLimitNs)) &&
+                     (t2 || mbar_wait(before, before_phase, abort_v, kWaitLimitNs));
+                ok = __all_sync(0xffffffffu, ok);
                 float v[32], top = -INFINITY;
+                if (ok) {
+                    const uint32_t mask = s_mask[s][half];
+                    uint32_t sv[32];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const float4 o = *reinterpret_cast<const float4 *>(recv + (half * 8 + c) * kHeads * 16 + head * 16);
-                    v[4 * c] = __uint_as_float(sv[4 * c]) + o.x;
-                    v[4 * c + 1] = __uint_as_float(sv[4 * c + 1]) + o.y;
-                    v[4 * c + 2] = __uint_as_float(sv[4 * c + 2]) + o.z;
-                    v[4 * c + 3] = __uint_as_float(sv[4 * c + 3]) + o.w;
+                    for (int c = 0; c < 2; ++c)
+                        tmem_ld_32x32b_x16(lanes + kTmemS + x * kTile + half * 32 + c * 16,
+                                           *reinterpret_cast<uint32_t(*)[16]>(&sv[c * 16]));
+                    float4 o[8];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        o[c] = *reinterpret_cast<const float4 *>(recv + x * kRecvBytes + (half * 8 + c) * kHeads * 16 + head * 16);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        v[4 * c] = (__uint_as_float(sv[4 * c]) + o[c].x) * scale2;
+                        v[4 * c + 1] = (__uint_as_float(sv[4 * c + 1]) + o[c].y) * scale2;
+                        v[4 * c + 2] = (__uint_as_float(sv[4 * c + 2]) + o[c].z) * scale2;
+                        v[4 * c + 3] = (__uint_as_float(sv[4 * c + 3]) + o[c].w) * scale2;
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.s_free[x]);
+                    if (mask != 0xffffffffu) {
+#pragma unroll
+                        for (int u = 0; u < 32; ++u) v[u] = (mask >> u) & 1u ? v[u] : -INFINITY;
+                    }
+                    float t4[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+                    for (int u = 4; u < 32; ++u) t4[u & 3] = fmaxf(t4[u & 3], v[u]);
+                    top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
                 }
-                __syncwarp();
-                if (lane == 0) arrive_cluster(peer_ok);
-                if (mask == 0xffffffffu) {
-#pragma unroll
-                    for (int u = 0; u < 32; ++u) v[u] *= scale2;
-                } else {
-#pragma unroll
-                    for (int u = 0; u < 32; ++u) v[u] = (mask >> u) & 1u ? v[u] * scale2 : -INFINITY;
-                }
-#pragma unroll
-                for (int u = 0; u < 32; ++u) top = fmaxf(top, v[u]);
-                s_max[half][head] = top;
-                // P V of the tile before is done with the weights' buffer and with O
-                if (j > 0) ok = ok && mbar_wait(&bars.kv_free[(g - 1) % kStages], ((g - 1) / kStages) & 1, abort_v, kWaitLimitNs);
-                if (!named_barrier_and(1, 32 * kSoftWarps, ok)) {
-                    ok = false;
-                    break;
-                }
-                top = fmaxf(s_max[0][head], s_max[1][head]);
-                const bool move = top > m + kLag;
-                if (__any_sync(0xffffffffu, move)) {
+                if (!named_barrier_and(1, 32 * kSoftWarps, ok && !(top > m + kLag))) {
+                    // a wait gave up, or a reference has to move
+                    s_max[half][head] = top;
+                    if (!named_barrier_and(1, 32 * kSoftWarps, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    top = fmaxf(s_max[0][head], s_max[1][head]);
                     const float mn = fmaxf(m, top);
                     const float f = exp2_approx(m - (mn == -INFINITY ? 0.f : mn));
                     m = mn;
                     l *= f;
-                    if (j > 0) {
+                    if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
                         tc_fence_after();
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
@@ -331,16 +397,19 @@ paged_attn_latent(const __grid_constant__ CUtensorMap qmap, AttnArgs a) {
                         }
                         tmem_st_wait();
                     }
+                    // the two halves of a head have both read s_max before either writes it again
+                    named_barrier(2 + quarter, 64);
                 }
                 const float ref = m == -INFINITY ? 0.f : m;
                 const uint32_t p = smem_u32(ps) + head * 128;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t hi4[4], lo4[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float p0 = exp2_approx(v[8 * c + 2 * e] - ref), p1 = exp2_approx(v[8 * c + 2 * e + 1] - ref);
-                        l += p0 + p1;
+                        sum[e] += p0 + p1;
                         const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
                         const float2 f = __bfloat1622float2(h);
                         const __nv_bfloat162 r = __floats2bfloat162_rn(p0 - f.x, p1 - f.y);
@@ -355,6 +424,7 @@ paged_attn_latent(const __grid_constant__ CUtensorMap qmap, AttnArgs a) {
                                  "r"(lo4[2]), "r"(lo4[3])
                                  : "memory");
                 }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
@@ -423,6 +493,12 @@ paged_attn_latent(const __grid_constant__ CUtensorMap qmap, AttnArgs a) {
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
     __syncthreads();
+    if (*abort_v) {
+        // scores that were sent and not waited for land well within this time
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 1000000) {}
+        __syncwarp();
+    }
     cluster_sync();           // nothing of the other CTA is on its way here any more
     if (warp == kMmaWarp) {
         tc_fence_after();
@@ -434,24 +510,6 @@ paged_attn_latent(const __grid_constant__ CUtensorMap qmap, AttnArgs a) {
     if (blockIdx.x == 0 && a.err)
         for (int b = threadIdx.x; b < a.B; b += blockDim.x)
             if (a.seq_len[b] > a.reach) raise_err(a.err, LSA_ERR_CAPACITY);
-}
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess) {
-            cudaGetLastError();
-            p = nullptr;
-        }
-        return reinterpret_cast<EncodeTiledFn>(p);
-    }();
-    return fn;
 }
 
 }  // namespace
@@ -470,26 +528,9 @@ AttnPlan plan_latent(const lsa_page_cache &c, int Hq) {
     return p;
 }
 
-lsa_status launch_latent(const lsa_page_cache &c, const AttnArgs &a, int grid, cudaStream_t st) {
-    EncodeTiledFn enc = encode_fn();
-    if (!enc) {
-        set_error("lsa_paged_attn: cuTensorMapEncodeTiled is unavailable");
-        return LSA_ERR_CUDA;
-    }
-    CUtensorMap qmap;
-    const cuuint32_t estr[3] = {1, 1, 1};
-    const cuuint64_t dims[3] = {cuuint64_t(kD), cuuint64_t(a.Hq), cuuint64_t(a.B)};
-    const cuuint64_t strides[2] = {cuuint64_t(kD) * 2, cuuint64_t(a.q_stride)};
-    const cuuint32_t box[3] = {64, kHeads, 1};
-    const CUresult r = enc(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.q), dims, strides, box, estr,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) {
-        set_error("lsa_paged_attn: cuTensorMapEncodeTiled failed (%d)", int(r));
-        return LSA_ERR_CUDA;
-    }
+lsa_status launch_latent(const AttnArgs &a, int grid, cudaStream_t st) {
     LSA_CUDA(ensure_smem(paged_attn_latent, kSmem));
-    LSA_CUDA(launch_pdl(paged_attn_latent, dim3(2 * grid), dim3(kThreads), kSmem, st, qmap, a));
+    LSA_CUDA(launch_pdl(paged_attn_latent, dim3(2 * grid), dim3(kThreads), kSmem, st, a));
     LSA_LAUNCHED("paged_attn_latent");
     return LSA_OK;
 }
