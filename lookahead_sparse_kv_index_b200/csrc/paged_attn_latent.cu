@@ -55,16 +55,51 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, uint3
 __device__ __forceinline__ void cp_async_arrive_noinc(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// Shared-memory descriptor of an MN-major operand with the 128-byte swizzle: 64-element blocks along MN `lbo` bytes
-// apart, 8-row groups along K 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_sw128_mn(uint32_t addr, uint32_t lbo) {
-    uint64_t d = 0;
-    d |= uint64_t((addr >> 4) & 0x3FFFu);
-    d |= uint64_t((lbo >> 4) & 0x3FFFu) << 16;
-    d |= uint64_t(1024 >> 4) << 32;
-    d |= uint64_t(1) << 46;
-    d |= uint64_t(2) << 61;
-    return d;
+// Low word of a shared-memory descriptor: start address and leading byte offset in 16-byte units.  K-major operands (P,
+// K) have 128-byte rows, whose leading offset is not used; V^T, the same rows read MN-major, has 64-element blocks along
+// its elements `lead` bytes apart.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead) {
+    return ((addr >> 4) & 0x3FFFu) | ((lead >> 4) & 0x3FFFu) << 16;
+}
+// High word: groups of 8 rows 1024 bytes apart, descriptor version for tcgen05, 128-byte swizzle.
+constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;
+// One lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
+    return r;
+}
+// D[tmem] (+)= A * B[smem]^T by the lane with `lead`, bf16 inputs, f32 accumulate: A in shared memory or in tensor memory.
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %6, 0;\n\t"
+        "mov.b64 a, {%1, %5};\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}\n"
+        ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %6, 0;\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}\n"
+        ::"r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t lead, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_u32(bar)),
+        "r"(lead)
+        : "memory");
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -85,16 +120,6 @@ __device__ __forceinline__ void st_async(uint32_t addr, uint32_t x, uint32_t y, 
 }
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// D[tmem] (+)= A[tmem] * B[smem]^T, bf16 inputs, f32 accumulate.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
-        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -196,41 +221,59 @@ paged_attn_latent(AttnArgs a) {
                 }
             }
         } else if (warp >= kLoadWarp) {
-            // ---- rows: lane l of warp w places row 32 w + l; the warp then copies its 32 rows, one a pass
-            const int w = warp - kLoadWarp;
+            // ---- rows: lane l of warp w places row 32 w + l (entry t, slot s of the sequence's page p; the page's index is
+            // read a tile ahead), then eight lanes copy a row, 16 bytes each of its four 128-byte blocks
+            const int w = warp - kLoadWarp, lr = lane >> 3, lp = lane & 7;
             const int32_t *row = a.table + int64_t(b) * a.table_stride;
-            const uint8_t *base = a.cache.k + kvh * a.cache.head_stride + rank * (kCols * 2) + lane * 16;
-            int64_t ahead = -1;
-            auto locate = [&](int j) {
-                const int t = lo + j * kTile + 32 * w + lane;
-                return j < n && t < hi ? entry_at(a, row, t).off : int64_t(-1);
-            };
-            ahead = locate(0);
+            const uint8_t *base = a.cache.k + kvh * a.cache.head_stride + rank * (kCols * 2) + lp * 16;
+            const int hop_p = kTile / a.cache.page_size, hop_s = kTile - hop_p * a.cache.page_size;
+            int t = lo + 32 * w + lane, p = t / a.cache.page_size, s_in = t - p * a.cache.page_size;
+            int64_t page = t < hi ? row[p] : -1;
             for (int j = 0; j < n; ++j) {
                 const uint32_t g = tiles + j, s = g % kStages;
+                int64_t off = -1;
+                if (t < hi) {
+                    if (page >= 0 && page < a.cache.n_pages)
+                        off = page * a.cache.page_stride + s_in * a.cache.slot_stride;
+                    else
+                        raise_err(a.err, LSA_ERR_INVALID);
+                }
+                t += kTile;
+                p += hop_p;
+                s_in += hop_s;
+                if (s_in >= a.cache.page_size) {
+                    s_in -= a.cache.page_size;
+                    ++p;
+                }
+                page = t < hi ? row[p] : -1;
                 if (g >= kStages && !mbar_wait(&bars.kv_free[s], (g / kStages - 1) & 1, abort_v, kWaitLimitNs)) break;
-                const uint32_t mask = __ballot_sync(0xffffffffu, ahead >= 0);
+                const uint32_t mask = __ballot_sync(0xffffffffu, off >= 0);
                 const uint32_t dst = smem_u32(kvs) + s * kStageBytes;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    // lane l copies piece l of the half row: piece l % 8 of column block l / 8
-                    const int r = 32 * w + i;
-                    const int64_t off = __shfl_sync(0xffffffffu, ahead, i);
-                    cp_async_16(dst + (lane >> 3) * kBlock + r * 128 + (((lane & 7) ^ (r & 7)) << 4),
-                                base + (off >= 0 ? off : 0), off >= 0 ? 16u : 0u);
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 32 * w + 4 * i + lr;
+                    const int64_t from = __shfl_sync(0xffffffffu, off, 4 * i + lr);
+                    const uint32_t bytes = from >= 0 ? 16u : 0u;
+                    const uint8_t *src = base + (from >= 0 ? from : 0);
+                    const uint32_t to = dst + r * 128 + ((lp ^ (r & 7)) << 4);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) cp_async_16(to + c * kBlock, src + c * 128, bytes);
                 }
                 cp_async_arrive_noinc(&bars.kv_full[s]);
                 if (lane == 0) {
                     s_mask[s][w] = mask;
                     mbar_arrive(&bars.mask_full[s]);
                 }
-                ahead = locate(j + 1);
             }
         } else if (warp == kMmaWarp) {
-            // ---- MMAs
-            if (lane == 0 && n > 0) {
+            // ---- MMAs.  The whole warp runs this, so that addresses are the same in all its lanes and stay in uniform
+            // registers, and one lane issues: from a branch of one lane each MMA took 85 cycles to issue
+            if (n > 0) {
                 constexpr uint32_t kIdescS = idesc_bf16(kHeads, kTile);
                 constexpr uint32_t kIdescO = idesc_bf16(kHeads, kCols) | (1u << 16);   // B (V) is MN-major
+                const uint32_t lead = elect_one();
+                const uint32_t kv_lo = desc_lo(smem_u32(kvs), 16), vt_lo = desc_lo(smem_u32(kvs), kBlock);
+                const uint32_t p_lo = desc_lo(smem_u32(ps), 16);
                 bool ok = mbar_wait(&bars.q_full, pieces & 1, abort_v, kWaitLimitNs);
                 auto s_tile = [&](int j) {
                     const uint32_t g = tiles + j, s = g % kStages;
@@ -238,34 +281,33 @@ paged_attn_latent(AttnArgs a) {
                     if (g >= 2 && !mbar_wait(&bars.s_free[g & 1], ((g >> 1) - 1) & 1, abort_v, kWaitLimitNs)) return false;
                     fence_proxy_async_smem();    // the rows were written by cp.async
                     tc_fence_after();
-                    const uint32_t kv = smem_u32(kvs) + s * kStageBytes;
+                    const uint32_t kv = kv_lo + s * (kStageBytes >> 4), d = tmem + kTmemS + (g & 1) * kTile;
 #pragma unroll
                     for (int i = 0; i < 16; ++i)      // 16 elements of K: 8 columns of Q
-                        mma_f16_ts(tmem + kTmemS + (g & 1) * kTile, tmem + kTmemQ + i * 8,
-                                   desc_sw128(kv + (i >> 2) * kBlock + (i & 3) * 32), kIdescS, i != 0);
-                    mma_commit(&bars.s_full[g & 1]);
+                        mma_ts(lead, d, tmem + kTmemQ + i * 8, kv + (i >> 2) * (kBlock >> 4) + (i & 3) * 2, kIdescS, i != 0);
+                    commit_if(lead, &bars.s_full[g & 1]);
                     return true;
                 };
-                ok = ok && s_tile(0) && (n < 2 || s_tile(1));
+                ok = __all_sync(0xffffffffu, ok && s_tile(0) && (n < 2 || s_tile(1)));
                 for (int j = 0; j < n && ok; ++j) {
                     if (j + 2 < n) ok = s_tile(j + 2);
                     const uint32_t g = tiles + j, s = g % kStages;
-                    ok = ok && mbar_wait(&bars.p_full, g & 1, abort_v, kWaitLimitNs);
+                    ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars.p_full, g & 1, abort_v, kWaitLimitNs));
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t p = smem_u32(ps), kv = smem_u32(kvs) + s * kStageBytes;
+                    const uint32_t vt = vt_lo + s * (kStageBytes >> 4);
 #pragma unroll
                     for (int x = 0; x < 2; ++x)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            mma_f16(tmem, desc_sw128(p + x * kPBytes + i * 32), desc_sw128_mn(kv + i * 2048, kBlock),
-                                    kIdescO, j != 0 || x != 0 || i != 0);
-                    mma_commit(&bars.kv_free[s]);
+                            mma_ss(lead, tmem, p_lo + x * (kPBytes >> 4) + i * 2, vt + i * (2048 >> 4), kIdescO,
+                                   x != 0 || i != 0 ? 1u : uint32_t(j != 0));
+                    commit_if(lead, &bars.kv_free[s]);
                 }
                 if (!ok) {
                     // what was issued still reads shared memory: let it end before the CTA does
                     volatile int none = 0;
-                    mma_commit(&bars.drain);
+                    commit_if(lead, &bars.drain);
                     mbar_wait(&bars.drain, 0, &none, kWaitLimitNs);
                 }
             }
@@ -348,17 +390,15 @@ paged_attn_latent(AttnArgs a) {
                     for (int c = 0; c < 2; ++c)
                         tmem_ld_32x32b_x16(lanes + kTmemS + x * kTile + half * 32 + c * 16,
                                            *reinterpret_cast<uint32_t(*)[16]>(&sv[c * 16]));
-                    float4 o[8];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        o[c] = *reinterpret_cast<const float4 *>(recv + x * kRecvBytes + (half * 8 + c) * kHeads * 16 + head * 16);
+                    const uint8_t *came = recv + x * kRecvBytes + (half * 8 * kHeads + head) * 16;
                     tmem_ld_wait();
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
-                        v[4 * c] = (__uint_as_float(sv[4 * c]) + o[c].x) * scale2;
-                        v[4 * c + 1] = (__uint_as_float(sv[4 * c + 1]) + o[c].y) * scale2;
-                        v[4 * c + 2] = (__uint_as_float(sv[4 * c + 2]) + o[c].z) * scale2;
-                        v[4 * c + 3] = (__uint_as_float(sv[4 * c + 3]) + o[c].w) * scale2;
+                        const float4 o = *reinterpret_cast<const float4 *>(came + c * kHeads * 16);
+                        v[4 * c] = (__uint_as_float(sv[4 * c]) + o.x) * scale2;
+                        v[4 * c + 1] = (__uint_as_float(sv[4 * c + 1]) + o.y) * scale2;
+                        v[4 * c + 2] = (__uint_as_float(sv[4 * c + 2]) + o.z) * scale2;
+                        v[4 * c + 3] = (__uint_as_float(sv[4 * c + 3]) + o.w) * scale2;
                     }
                     tc_fence_before();
                     __syncwarp();
