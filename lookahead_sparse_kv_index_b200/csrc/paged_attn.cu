@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads) paged_attn_cc(AttnArgs a, int stages
             if (a.seq_len[b] > a.reach) raise_err(a.err, LSA_ERR_CAPACITY);
 }
 
-// Joins a segment's partials (paged_attn.cuh): CTA (c, i) those of CTA c's record, for head i of the group.  A group of
+// Joins a segment's partials (paged_attn.cuh): CTA (r, i) those of record r, for head i of the group.  A group of
 // D / 4 threads adds 16-byte pieces of every kGroups-th partial; its first loads are on their way while the weights are
 // made.
 constexpr int kCombineThreads = 256, kAhead = 4;
@@ -197,13 +197,13 @@ __global__ void __launch_bounds__(kCombineThreads) paged_attn_combine(AttnArgs a
     __shared__ float red[2][kCombineThreads / 32];
     __shared__ float4 sums[kCombineThreads];
     extern __shared__ float wgt[];   // [grid]
-    const int c = blockIdx.x, h = blockIdx.y, D = a.cache.D, HS = a.HS;
+    const int h = blockIdx.y, D = a.cache.D, HS = a.HS;
     pdl_launch_dependents();
     pdl_wait();
-    const Record rec = a.records[c];
+    const Record rec = a.records[blockIdx.x];
     const int in = (rec.hseg % a.HG) * HS + h;
     if (rec.b < 0 || in >= a.G) return;
-    const int P = rec.last - c + 1;
+    const int c = rec.first, P = rec.last - c + 1;
     auto slot = [&](int p) { return int64_t(p == 0 ? 2 * c + 1 : 2 * (c + p)) * HS + h; };
     const int lanes = D / 4, groups = kCombineThreads / lanes, lane4 = threadIdx.x % lanes, grp = threadIdx.x / lanes;
     float4 ahead[kAhead];
@@ -362,7 +362,8 @@ lsa_status check_cache(const lsa_page_cache *c, const char *who) {
 
 lsa_status paged_combine(const AttnArgs &a, int grid, cudaStream_t st) {
     const int heads = a.HS < a.G ? a.HS : a.G;
-    LSA_CUDA(launch_pdl(paged_attn_combine, dim3(grid, heads), dim3(kCombineThreads), size_t(grid) * 4, st, a));
+    const int records = a.by_segment ? a.B * a.cache.Hkv * a.HG : grid;
+    LSA_CUDA(launch_pdl(paged_attn_combine, dim3(records, heads), dim3(kCombineThreads), size_t(grid) * 4, st, a));
     LSA_LAUNCHED("paged_attn_combine");
     return LSA_OK;
 }
@@ -451,6 +452,7 @@ extern "C" lsa_status lsa_paged_attn(const void *Q, lsa_dtype q_dtype, int64_t q
     const int64_t segments = int64_t(B) * cache->Hkv * p.HG;
     a.whole = most <= int64_t(kWholeUnits) * p.tile && segments < (int64_t(1) << 31);
     const int grid = a.whole ? int(segments) : p.grid;
+    a.by_segment = segments <= grid;
     cudaStream_t st = as_stream(stream);
     s = cache->dtype == LSA_F32 ? dispatch_cc(a, p, grid, st)
         : latent_supported(*cache, Hq) ? launch_latent(a, grid, st) : launch_mma(*cache, a, p, grid, st);

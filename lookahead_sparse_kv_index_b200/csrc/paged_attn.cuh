@@ -10,7 +10,8 @@
 // for 2^x), and the combine kernel joins a segment's partials in unit order:
 //     M = max m_c,  L = sum l_c 2^(m_c - M),  o = sum o_c 2^(m_c - M) / L,  lse = (M + log2 L) ln 2.
 // A CTA has at most two partials: slot 2c for the piece that continues a segment, 2c + 1 for one that begins it; where
-// it begins one, it records which (a record a CTA), and the record's combine CTAs join it.
+// it begins one, it records which, and the record's combine CTAs join it.  There is a record for each CTA, or for each
+// segment where these are fewer.
 #pragma once
 
 #include "paged.cuh"
@@ -18,9 +19,9 @@
 namespace lsa {
 namespace paged {
 
-// A segment that CTA c begins and the CTAs up to `last` continue (b < 0: none).
+// A segment that CTA `first` begins and the CTAs up to `last` continue (b < 0: none).
 struct alignas(16) Record {
-    int32_t b, hseg, last, unused;
+    int32_t b, hseg, first, last;
 };
 
 struct AttnArgs {
@@ -38,7 +39,8 @@ struct AttnArgs {
     void *out;
     float *lse;
     float *part_o, *part_ml;     // [2 * grid][HS][D], [2 * grid][HS][2]
-    Record *records;             // [grid]
+    Record *records;             // [grid], or [segments]
+    int32_t by_segment;
     int32_t *err;
     int32_t tile, lead;
     int32_t whole;               // 1: CTA c does segment c and no partials are written
@@ -160,10 +162,12 @@ __device__ __forceinline__ void for_pieces(const AttnArgs &a, int cta, int ctas,
         f(b, cta - b * heads, s.lo, s.hi, -1);
         return;
     }
-    if (threadIdx.x == 0) a.records[cta] = Record{-1, 0, 0, 0};
+    if (threadIdx.x == 0 && !a.by_segment) a.records[cta] = Record{-1, 0, 0, 0};
     // sequences without entries have no units
     for (int e = cta; e < a.B; e += ctas) {
         if (tiles_of(a, e) != 0) continue;
+        if (a.by_segment)
+            for (int i = threadIdx.x; i < heads; i += blockDim.x) a.records[e * heads + i] = Record{-1, 0, 0, 0};
         for (int64_t i = threadIdx.x; i < int64_t(a.Hq) * a.cache.D; i += blockDim.x)
             store_out(a, int64_t(e) * a.Hq * a.cache.D + i, 0.f);
         if (a.lse)
@@ -187,8 +191,9 @@ __device__ __forceinline__ void for_pieces(const AttnArgs &a, int cta, int ctas,
         const int t0 = max(at - a.lead, 0), t1 = max(at + take - a.lead, 0);
         if (t1 > t0) {
             const int lo = s.lo + t0 * a.tile, hi = t1 == n ? s.hi : s.lo + t1 * a.tile;
-            if (t0 == 0 && t1 < n && threadIdx.x == 0)
-                a.records[cta] = Record{b, hseg, int32_t((u - at + units - 1) / w.share), 0};
+            if (t0 == 0 && threadIdx.x == 0 && (t1 < n || a.by_segment))
+                a.records[a.by_segment ? b * heads + hseg : cta] =
+                    Record{t1 < n ? b : -1, hseg, cta, int32_t((u - at + units - 1) / w.share)};
             f(b, hseg, lo, hi, t0 == 0 && t1 == n ? -1 : 2 * cta + (t0 == 0));
         }
         u += take;

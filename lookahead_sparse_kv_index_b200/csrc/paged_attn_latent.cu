@@ -12,14 +12,15 @@
 //   * P enters as two bf16 numbers (a weight and what its rounding left), as in paged_attn_mma.cu.
 // Tensor memory: O in columns 0 .. 255, two buffers of S in 256 .. 383, Q_r (bf16, the MMA's A operand) in 384 .. 511;
 // Q there leaves shared memory to four tiles of rows (32 KB each), P (2 x 16 KB) and two buffers of the other's S.
-// Twelve warps: 0-7 softmax (thread = head, half of the tile's entries), 8 issues the MMAs, 9-10 copy rows (cp.async),
-// 11 tells the other CTA what was read of its scores (a release that would hold the softmax up for 350 cycles a tile).
+// Sixteen warps: 0-7 softmax (thread = head, half of the tile's entries), 8-11 send S_r, 12 issues the MMAs, 13-14 copy
+// rows (cp.async), 15 tells the other CTA what was read of its scores.  Sending and telling have warps of their own
+// because they are slow and nothing depends on them at once: the 32 KB of a tile cross in about 1300 cycles, and a
+// release at cluster scope takes 350.
 // A tile passes load, S, exchange, softmax, P V; what counts is that these overlap.  S of tile i + 2 is issued as soon as
-// the scores of tile i are in registers, before P V of tile i, and the softmax warps send their S of tile i + 1 before
-// they take up what came for tile i, so neither the exchange nor a product is waited for (with S of tile i + 1 issued
-// after P V of tile i - 1 the softmax and the tensor pipe took turns: 423 us for 128 heads over 4 x 131072 entries).  The
-// running max is a reference that moves, and O is rescaled, only when a score passes it by 2^8; a barrier that every
-// tile needs anyway tells whether one did.  Every wait is bounded; the two CTAs leave together.
+// the scores of tile i are in registers, before P V of tile i, so neither the exchange nor a product is waited for (with
+// S of tile i + 1 issued after P V of tile i - 1 the softmax and the tensor pipe took turns: 423 us for 128 heads over
+// 4 x 131072 entries).  The running max is a reference that moves, and O is rescaled, only when a score passes it by 2^8;
+// a barrier that every tile needs anyway tells whether one did.  Every wait is bounded; the two CTAs leave together.
 #include "paged_attn.cuh"
 #include "tc_ptx.cuh"
 
@@ -30,7 +31,7 @@ namespace {
 using namespace ptx;
 
 constexpr int kHeads = 128, kD = 512, kCols = 256, kTile = 64, kStages = 4;
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kLoadWarps = 2, kAckWarp = 11;
+constexpr int kSoftWarps = 8, kSendWarp = 8, kSendWarps = 4, kMmaWarp = 12, kLoadWarp = 13, kLoadWarps = 2, kAckWarp = 15;
 constexpr int kThreads = 32 * (kAckWarp + 1);
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr int kTmemS = kCols, kTmemQ = kCols + 2 * kTile;
@@ -186,12 +187,15 @@ paged_attn_latent(AttnArgs a) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bars.s_full[s], 1);
             mbar_init(&bars.s_recv[s], 1);
-            mbar_init(&bars.s_free[s], kSoftWarps);
+            mbar_init(&bars.s_free[s], kSoftWarps + kSendWarps);
             mbar_init(&bars.send_ok[s], 1);
         }
         mbar_init(&bars.p_full, kSoftWarps);
         mbar_init(&bars.drain, 1);
         fence_mbar_init();
+        // a tile's scores from the other CTA: a buffer's next tile is announced when one has come
+        mbar_arrive_expect_tx(&bars.s_recv[0], kRecvBytes);
+        mbar_arrive_expect_tx(&bars.s_recv[1], kRecvBytes);
     }
     if (warp == kMmaWarp) {
         tmem_alloc(&tmem_slot, 512);
@@ -311,37 +315,39 @@ paged_attn_latent(AttnArgs a) {
                     mbar_wait(&bars.drain, 0, &none, kWaitLimitNs);
                 }
             }
+        } else if (warp >= kSendWarp) {
+            // ---- S_r of each tile to the other CTA: thread = head, 16 pieces of four entries
+            const int quarter = warp & 3, head = 32 * quarter + lane;
+            const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
+            const uint32_t peer_slot = in_cta(smem_u32(recv) + head * 16, peer);
+            const uint32_t peer_recv = in_cta(smem_u32(&bars.s_recv[0]), peer);
+            for (int j = 0; j < n; ++j) {
+                const uint32_t g = tiles + j, x = g & 1;
+                bool ok = mbar_wait(&bars.s_full[x], (g >> 1) & 1, abort_v, kWaitLimitNs);
+                // the other CTA has read tile g - 2, which lay there
+                ok = ok && (g < 2 || wait_cluster(&bars.send_ok[x], ((g >> 1) - 1) & 1, abort_v));
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tc_fence_after();
+                uint32_t sv[64];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    tmem_ld_32x32b_x16(lanes + kTmemS + x * kTile + c * 16, *reinterpret_cast<uint32_t(*)[16]>(&sv[c * 16]));
+                tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.s_free[x]);
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    st_async(peer_slot + x * kRecvBytes + c * kHeads * 16, sv[4 * c], sv[4 * c + 1], sv[4 * c + 2],
+                             sv[4 * c + 3], peer_recv + x * 8);
+            }
         } else {
             // ---- softmax: thread = head 32 * quarter + lane, entries 32 * half .. of each tile
             const int quarter = warp & 3, half = warp >> 2, head = 32 * quarter + lane;
             const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
             const float scale2 = a.scale * kLog2e;
-            const uint32_t slot_at = smem_u32(recv) + (half * 8 * kHeads + head) * 16;   // of 8 pieces, kHeads * 16 apart
-            const uint32_t peer_slot = in_cta(slot_at, peer), peer_recv = in_cta(smem_u32(&bars.s_recv[0]), peer);
             float m = -INFINITY, l = 0.f;
             bool ok = true;
-            // S_r of tile j to the other CTA
-            auto send = [&](int j) {
-                const uint32_t g = tiles + j, x = g & 1;
-                if (threadIdx.x == 0) mbar_arrive_expect_tx(&bars.s_recv[x], kRecvBytes);   // for what comes here
-                bool sent = mbar_wait(&bars.s_full[x], (g >> 1) & 1, abort_v, kWaitLimitNs);
-                // the other CTA has read tile g - 2, which lay there
-                if (g >= 2) sent = wait_cluster(&bars.send_ok[x], ((g >> 1) - 1) & 1, abort_v) && sent;
-                sent = __all_sync(0xffffffffu, sent);
-                if (!sent) return false;
-                tc_fence_after();
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t sv[16];
-                    tmem_ld_32x32b_x16(lanes + kTmemS + x * kTile + half * 32 + c * 16, sv);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        st_async(peer_slot + x * kRecvBytes + (4 * c + y) * kHeads * 16, sv[4 * y], sv[4 * y + 1],
-                                 sv[4 * y + 2], sv[4 * y + 3], peer_recv + x * 8);
-                }
-                return true;
-            };
             if (n > 0) {
                 // Q_r: this thread's head, 128 of the 256 columns, two to a column of tensor memory
                 const int heads = min(kHeads, a.G - first);
@@ -365,23 +371,25 @@ paged_attn_latent(AttnArgs a) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.q_full);
-                ok = send(0);
             }
             for (int j = 0; j < n; ++j) {
                 const uint32_t g = tiles + j, s = g % kStages, x = g & 1;
-                if (j + 1 < n) ok = send(j + 1) && ok;
-                // three waits, tried together (each takes a hundred cycles even when there is nothing to wait for): the
+                // four waits, tried together (each takes a hundred cycles even when there is nothing to wait for): S_r, the
                 // other CTA's scores, which rows are there, and P V of the tile before, which is done with the weights'
                 // buffer and with O
                 uint64_t *before = &bars.kv_free[(g + kStages - 1) % kStages];
                 const uint32_t before_phase = ((g - 1) / kStages) & 1;
+                const bool t3 = mbar_try_wait(&bars.s_full[x], (g >> 1) & 1);
                 const bool t0 = try_cluster(&bars.s_recv[x], (g >> 1) & 1);
                 const bool t1 = mbar_try_wait(&bars.mask_full[s], (g / kStages) & 1);
                 const bool t2 = j == 0 || mbar_try_wait(before, before_phase);
                 ok = ok && (t0 || wait_cluster(&bars.s_recv[x], (g >> 1) & 1, abort_v)) &&
                      (t1 || mbar_wait(&bars.mask_full[s], (g / kStages) & 1, abort_v, kWaitLimitNs)) &&
-                     (t2 || mbar_wait(before, before_phase, abort_v, kWaitLimitNs));
+                     (t2 || mbar_wait(before, before_phase, abort_v, kWaitLimitNs)) &&
+                     (t3 || mbar_wait(&bars.s_full[x], (g >> 1) & 1, abort_v, kWaitLimitNs));
                 ok = __all_sync(0xffffffffu, ok);
+                if (ok) tc_fence_after();
+                if (ok && threadIdx.x == 0) mbar_arrive_expect_tx(&bars.s_recv[x], kRecvBytes);
                 float v[32], top = -INFINITY;
                 if (ok) {
                     const uint32_t mask = s_mask[s][half];
