@@ -374,22 +374,22 @@ paged_attn_latent(AttnArgs a) {
             }
             for (int j = 0; j < n; ++j) {
                 const uint32_t g = tiles + j, s = g % kStages, x = g & 1;
-                // four waits, tried together (each takes a hundred cycles even when there is nothing to wait for): S_r, the
-                // other CTA's scores, which rows are there, and P V of the tile before, which is done with the weights'
-                // buffer and with O
-                uint64_t *before = &bars.kv_free[(g + kStages - 1) % kStages];
-                const uint32_t before_phase = ((g - 1) / kStages) & 1;
-                const bool t3 = mbar_try_wait(&bars.s_full[x], (g >> 1) & 1);
-                const bool t0 = try_cluster(&bars.s_recv[x], (g >> 1) & 1);
+                // three waits, tried together (each takes a hundred cycles even when there is nothing to wait for): S_r, the
+                // other CTA's scores, and which rows are there
+                const bool t0 = mbar_try_wait(&bars.s_full[x], (g >> 1) & 1);
                 const bool t1 = mbar_try_wait(&bars.mask_full[s], (g / kStages) & 1);
-                const bool t2 = j == 0 || mbar_try_wait(before, before_phase);
-                ok = ok && (t0 || wait_cluster(&bars.s_recv[x], (g >> 1) & 1, abort_v)) &&
+                const bool t2 = try_cluster(&bars.s_recv[x], (g >> 1) & 1);
+                ok = ok && (t0 || mbar_wait(&bars.s_full[x], (g >> 1) & 1, abort_v, kWaitLimitNs)) &&
                      (t1 || mbar_wait(&bars.mask_full[s], (g / kStages) & 1, abort_v, kWaitLimitNs)) &&
-                     (t2 || mbar_wait(before, before_phase, abort_v, kWaitLimitNs)) &&
-                     (t3 || mbar_wait(&bars.s_full[x], (g >> 1) & 1, abort_v, kWaitLimitNs));
+                     (t2 || wait_cluster(&bars.s_recv[x], (g >> 1) & 1, abort_v));
                 ok = __all_sync(0xffffffffu, ok);
                 if (ok) tc_fence_after();
                 if (ok && threadIdx.x == 0) mbar_arrive_expect_tx(&bars.s_recv[x], kRecvBytes);
+                // P V of the tile before: when it is done, the weights' buffer is free and O is whole
+                auto before_done = [&]() {
+                    return j == 0 || mbar_wait(&bars.kv_free[(g + kStages - 1) % kStages], ((g - 1) / kStages) & 1, abort_v,
+                                               kWaitLimitNs);
+                };
                 float v[32], top = -INFINITY;
                 if (ok) {
                     const uint32_t mask = s_mask[s][half];
@@ -423,6 +423,7 @@ paged_attn_latent(AttnArgs a) {
                 if (!named_barrier_and(1, 32 * kSoftWarps, ok && !(top > m + kLag))) {
                     // a wait gave up, or a reference has to move
                     s_max[half][head] = top;
+                    ok = ok && before_done();
                     if (!named_barrier_and(1, 32 * kSoftWarps, ok)) {
                         ok = false;
                         break;
@@ -451,25 +452,27 @@ paged_attn_latent(AttnArgs a) {
                 const float ref = m == -INFINITY ? 0.f : m;
                 const uint32_t p = smem_u32(ps) + head * 128;
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                uint32_t near[16], rest[16];      // the weights, and what their rounding left
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float p0 = exp2_approx(v[2 * e] - ref), p1 = exp2_approx(v[2 * e + 1] - ref);
+                    sum[e & 3] += p0 + p1;
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
+                    const float2 f = __bfloat1622float2(h);
+                    const __nv_bfloat162 r = __floats2bfloat162_rn(p0 - f.x, p1 - f.y);
+                    near[e] = *reinterpret_cast<const uint32_t *>(&h);
+                    rest[e] = *reinterpret_cast<const uint32_t *>(&r);
+                }
+                // (a wait that gives up here shows at the next tile's barrier, or at the piece's end)
+                ok = before_done();
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    uint32_t hi4[4], lo4[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float p0 = exp2_approx(v[8 * c + 2 * e] - ref), p1 = exp2_approx(v[8 * c + 2 * e + 1] - ref);
-                        sum[e] += p0 + p1;
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
-                        const float2 f = __bfloat1622float2(h);
-                        const __nv_bfloat162 r = __floats2bfloat162_rn(p0 - f.x, p1 - f.y);
-                        hi4[e] = *reinterpret_cast<const uint32_t *>(&h);
-                        lo4[e] = *reinterpret_cast<const uint32_t *>(&r);
-                    }
                     const uint32_t at = p + (((4 * half + c) ^ (head & 7)) << 4);
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(hi4[0]), "r"(hi4[1]),
-                                 "r"(hi4[2]), "r"(hi4[3])
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(near[4 * c]), "r"(near[4 * c + 1]),
+                                 "r"(near[4 * c + 2]), "r"(near[4 * c + 3])
                                  : "memory");
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + kPBytes), "r"(lo4[0]), "r"(lo4[1]),
-                                 "r"(lo4[2]), "r"(lo4[3])
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + kPBytes), "r"(rest[4 * c]),
+                                 "r"(rest[4 * c + 1]), "r"(rest[4 * c + 2]), "r"(rest[4 * c + 3])
                                  : "memory");
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
