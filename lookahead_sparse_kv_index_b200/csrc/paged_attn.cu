@@ -1,193 +1,14 @@
 // Attention of one new token per sequence over a paged key-value cache (lsa_paged_attn):
 //     a_t = scale q . K_t,   out = sum_t softmax(a)_t V_t,   lse = log sum_t exp(a_t).
 //
-// This file holds the entry point, the kernel of fp32 rows and the combine; bf16 and e4m3 rows are paged_attn_mma.cu's.
+// This file holds the entry point and the combine; the kernels are paged_attn_mma.cu's (bf16 and e4m3 rows),
+// paged_attn_latent.cu's (a bf16 latent head of 512 under more than 8 query heads) and paged_attn_f32.cu's.
 // paged_attn.cuh says how the work is cut.
-//
-// The kernel of fp32 rows runs on the CUDA cores (the tensor cores have no fp32 product): a CTA of 8 warps stages `tile` entries of K and V at a time in shared memory
-// through a ring of cp.async stages.  Eight lanes share an entry (each D / 8 of its elements, 16-byte pieces), so a
-// warp holds four entries; every group of eight lanes runs its own online softmax over its entries (max m, sum l and
-// o in registers) for NH query heads, the warps split first the heads and then the entries, and the parts meet once,
-// at the end of a piece.
 #include "paged_attn.cuh"
 
 namespace lsa {
 namespace paged {
 namespace {
-
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kRing = 8;             // tiles whose row offsets are kept: more than any stage count + 1
-constexpr int kMaxTile = 32;
-
-__device__ __forceinline__ uint32_t smem_addr(const void *p) { return uint32_t(__cvta_generic_to_shared(p)); }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void cp_wait(int left) {
-    if (left <= 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
-    else if (left == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else asm volatile("cp.async.wait_group 2;" ::: "memory");
-}
-
-__device__ __forceinline__ float4 load4(const uint8_t *row, int chunk) {
-    return *reinterpret_cast<const float4 *>(row + chunk * 16);
-}
-
-// KC: 4-element chunks of a lane (D <= 32 KC); NH: query heads of a warp.
-template <int KC, int NH>
-__global__ void __launch_bounds__(kThreads) paged_attn_cc(AttnArgs a, int stages, int nhg) {
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t scratch[40];
-    __shared__ Entry ring[kRing][kMaxTile];
-    const int D = a.cache.D, HS = a.HS, tile = a.tile;
-    const bool latent = a.cache.v == a.cache.k;
-    const int row_bytes = D * 4, nch = row_bytes / 16;
-    const int stage_bytes = tile * row_bytes * (latent ? 1 : 2);
-    float *qs = reinterpret_cast<float *>(smem + size_t(stages) * stage_bytes);   // [HS][D]
-    float *po = qs + HS * D;                                                      // [TS][HS][D]
-    const int TS = kWarps / nhg;
-    float *pml = po + TS * HS * D;                                                // [TS][HS][2]
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = lane >> 3, dl = lane & 7;
-    const int hw = (warp % nhg) * NH, ts = warp / nhg;
-    const float scale2 = a.scale * kLog2e;
-
-    pdl_launch_dependents();
-    pdl_wait();
-    for_pieces(a, blockIdx.x, gridDim.x, scratch, [&](int b, int hseg, int lo, int hi, int slot) {
-        const int kvh = hseg / a.HG, first = (hseg % a.HG) * HS;
-        const int32_t *row = a.table + int64_t(b) * a.table_stride;
-        const int ntiles = (hi - lo + tile - 1) / tile;
-        const uint8_t *kbase = a.cache.k + kvh * a.cache.head_stride, *vbase = a.cache.v + kvh * a.cache.head_stride;
-
-        auto locate = [&](int j) {   // row offsets of tile j
-            if (threadIdx.x < tile && j < ntiles) {
-                const int t = lo + j * tile + threadIdx.x;
-                ring[j % kRing][threadIdx.x] = t < hi ? entry_at(a, row, t) : Entry{-1, 0};
-            }
-        };
-        auto issue = [&](int j) {
-            if (j < ntiles) {
-                const uint32_t st = smem_addr(smem) + uint32_t(j % stages) * stage_bytes;
-                for (int i = threadIdx.x; i < tile * nch; i += kThreads) {
-                    const int r = i / nch, c = i - r * nch;
-                    const Entry e = ring[j % kRing][r];
-                    const bool ok = e.off >= 0;
-                    cp_async16(st + r * row_bytes + c * 16, kbase + (ok ? e.off : 0) + c * 16, ok);
-                    if (!latent)
-                        cp_async16(st + (tile + r) * row_bytes + c * 16, vbase + (ok ? e.off : 0) + c * 16, ok);
-                }
-            }
-            cp_commit();
-        };
-
-        for (int i = threadIdx.x; i < HS * D; i += kThreads) {
-            const int h = i / D, d = i - h * D;
-            float v = 0.f;
-            if (first + h < a.G) {
-                const int64_t at = (int64_t(kvh) * a.G + first + h) * D + d;
-                const uint8_t *q = static_cast<const uint8_t *>(a.q) + int64_t(b) * a.q_stride;
-                v = reinterpret_cast<const float *>(q)[at];
-            }
-            qs[i] = v;
-        }
-        for (int j = 0; j < stages; ++j) locate(j);
-        __syncthreads();
-        for (int j = 0; j < stages - 1; ++j) issue(j);
-
-        float m[NH], l[NH], o[NH][KC * 4];
-#pragma unroll
-        for (int h = 0; h < NH; ++h) {
-            m[h] = -INFINITY;
-            l[h] = 0.f;
-#pragma unroll
-            for (int e = 0; e < KC * 4; ++e) o[h][e] = 0.f;
-        }
-        for (int i = 0; i < ntiles; ++i) {
-            cp_wait(stages - 2);
-            __syncthreads();
-            issue(i + stages - 1);
-            locate(i + stages);
-            const uint8_t *st = smem + size_t(i % stages) * stage_bytes;
-            const uint8_t *sv = latent ? st : st + tile * row_bytes;
-            for (int t0 = ts * 4; t0 < tile; t0 += TS * 4) {
-                const int t = min(t0 + grp, tile - 1);
-                const bool ok = t0 + grp < tile && ring[i % kRing][t].off >= 0;
-                float dot[NH];
-#pragma unroll
-                for (int h = 0; h < NH; ++h) dot[h] = 0.f;
-#pragma unroll
-                for (int c = 0; c < KC; ++c) {
-                    const int ch = c * 8 + dl;
-                    if (ch * 4 < D) {
-                        const float4 kx = load4(st + t * row_bytes, ch);
-#pragma unroll
-                        for (int h = 0; h < NH; ++h) {
-                            const float4 q = *reinterpret_cast<const float4 *>(qs + (hw + h) * D + ch * 4);
-                            dot[h] = fmaf(q.x, kx.x, fmaf(q.y, kx.y, fmaf(q.z, kx.z, fmaf(q.w, kx.w, dot[h]))));
-                        }
-                    }
-                }
-                float4 vx[KC];
-#pragma unroll
-                for (int c = 0; c < KC; ++c) {
-                    const int ch = c * 8 + dl;
-                    vx[c] = ch * 4 < D ? load4(sv + t * row_bytes, ch) : make_float4(0.f, 0.f, 0.f, 0.f);
-                }
-#pragma unroll
-                for (int h = 0; h < NH; ++h) {
-                    float s = dot[h];
-#pragma unroll
-                    for (int x = 1; x < 8; x <<= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-                    s = ok ? s * scale2 : -INFINITY;
-                    const float mn = fmaxf(m[h], s), ref = mn == -INFINITY ? 0.f : mn;
-                    const float f = exp2_approx(m[h] - ref);
-                    const float p = ok ? exp2_approx(s - ref) : 0.f;
-                    m[h] = mn;
-                    l[h] = fmaf(l[h], f, p);
-#pragma unroll
-                    for (int c = 0; c < KC; ++c) {
-                        o[h][c * 4] = fmaf(p, vx[c].x, o[h][c * 4] * f);
-                        o[h][c * 4 + 1] = fmaf(p, vx[c].y, o[h][c * 4 + 1] * f);
-                        o[h][c * 4 + 2] = fmaf(p, vx[c].z, o[h][c * 4 + 2] * f);
-                        o[h][c * 4 + 3] = fmaf(p, vx[c].w, o[h][c * 4 + 3] * f);
-                    }
-                }
-            }
-        }
-        cp_wait(0);
-        // join the warp's four groups, then leave the warp's part in shared memory
-#pragma unroll
-        for (int h = 0; h < NH; ++h) {
-            float M = m[h];
-            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 8));
-            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
-            const float f = exp2_approx(m[h] - (M == -INFINITY ? 0.f : M));
-            float L = l[h] * f;
-            L += __shfl_xor_sync(0xffffffffu, L, 8);
-            L += __shfl_xor_sync(0xffffffffu, L, 16);
-#pragma unroll
-            for (int e = 0; e < KC * 4; ++e) {
-                float v = o[h][e] * f;
-                v += __shfl_xor_sync(0xffffffffu, v, 8);
-                v += __shfl_xor_sync(0xffffffffu, v, 16);
-                const int d = ((e >> 2) * 8 + dl) * 4 + (e & 3);
-                if (grp == 0 && d < D) po[(ts * HS + hw + h) * D + d] = v;
-            }
-            if (lane == 0) {
-                pml[(ts * HS + hw + h) * 2] = M;
-                pml[(ts * HS + hw + h) * 2 + 1] = L;
-            }
-        }
-        __syncthreads();
-        finish_piece(a, b, hseg, slot, TS, po, pml);
-        __syncthreads();
-    });
-    if (blockIdx.x == 0 && a.err)
-        for (int b = threadIdx.x; b < a.B; b += kThreads)
-            if (a.seq_len[b] > a.reach) raise_err(a.err, LSA_ERR_CAPACITY);
-}
 
 // Joins a segment's partials (paged_attn.cuh): CTA (r, i) those of record r, for head i of the group.  A group of
 // D / 4 threads adds 16-byte pieces of every kGroups-th partial; its first loads are on their way while the weights are
@@ -266,61 +87,8 @@ __global__ void __launch_bounds__(kCombineThreads) paged_attn_combine(AttnArgs a
     if (threadIdx.x == 0 && a.lse) a.lse[hq] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
-int ceil_pow2(int x) {
-    int p = 1;
-    while (p < x) p *= 2;
-    return p;
-}
-
-// KC of a head dim, and the heads of a warp that keep o within 64 registers.
-int cc_chunks(int D) {
-    const int need = (D + 31) / 32;
-    for (int k : {1, 2, 3, 4, 6, 8})
-        if (need <= k) return k;
-    return 16;
-}
-int cc_heads(int kc) { return kc <= 2 ? 8 : kc <= 4 ? 4 : kc <= 8 ? 2 : 1; }
-
-AttnPlan plan_cc(const lsa_page_cache &c, int Hq) {
-    AttnPlan p = {};
-    const int G = Hq / c.Hkv, nh = cc_heads(cc_chunks(c.D));
-    const int nhg = ceil_pow2(G >= kWarps * nh ? kWarps : (G + nh - 1) / nh);
-    p.HS = nhg * nh;
-    p.HG = (G + p.HS - 1) / p.HS;
-    const size_t entry = size_t(c.D) * 4 * (c.v == c.k ? 1 : 2);
-    p.tile = kMaxTile;
-    while (p.tile > 4 && p.tile * entry > 24 * 1024) p.tile /= 2;
-    p.lead = 6;
-    p.stages = 4;
-    p.threads = kThreads;
-    p.smem = p.stages * p.tile * entry + (size_t(p.HS) * c.D + size_t(kWarps / nhg) * p.HS * (c.D + 2)) * 4;
-    p.grid = sm_count() * 2;
-    return p;
-}
-
-template <int KC, int NH>
-lsa_status launch_cc(const AttnArgs &a, const AttnPlan &p, int grid, cudaStream_t st) {
-    LSA_CUDA(ensure_smem(paged_attn_cc<KC, NH>, p.smem));
-    LSA_CUDA(launch_pdl(paged_attn_cc<KC, NH>, dim3(grid), dim3(kThreads), p.smem, st, a, int(p.stages),
-                        int(p.HS / NH)));
-    LSA_LAUNCHED("paged_attn_cc");
-    return LSA_OK;
-}
-
-lsa_status dispatch_cc(const AttnArgs &a, const AttnPlan &p, int grid, cudaStream_t st) {
-    switch (cc_chunks(a.cache.D)) {
-    case 1: return launch_cc<1, 8>(a, p, grid, st);
-    case 2: return launch_cc<2, 8>(a, p, grid, st);
-    case 3: return launch_cc<3, 4>(a, p, grid, st);
-    case 4: return launch_cc<4, 4>(a, p, grid, st);
-    case 6: return launch_cc<6, 2>(a, p, grid, st);
-    case 8: return launch_cc<8, 2>(a, p, grid, st);
-    default: return launch_cc<16, 1>(a, p, grid, st);
-    }
-}
-
 AttnPlan plan_of(const lsa_page_cache &c, int Hq) {
-    if (c.dtype == LSA_F32) return plan_cc(c, Hq);
+    if (c.dtype == LSA_F32) return plan_f32(c, Hq);
     return latent_supported(c, Hq) ? plan_latent(c, Hq) : plan_mma(c, Hq);
 }
 
@@ -454,7 +222,7 @@ extern "C" lsa_status lsa_paged_attn(const void *Q, lsa_dtype q_dtype, int64_t q
     const int grid = a.whole ? int(segments) : p.grid;
     a.by_segment = segments <= grid;
     cudaStream_t st = as_stream(stream);
-    s = cache->dtype == LSA_F32 ? dispatch_cc(a, p, grid, st)
+    s = cache->dtype == LSA_F32 ? launch_f32(a, p, grid, st)
         : latent_supported(*cache, Hq) ? launch_latent(a, grid, st) : launch_mma(*cache, a, p, grid, st);
     if (s != LSA_OK || a.whole) return s;
     return paged_combine(a, grid, st);

@@ -237,6 +237,9 @@ struct AttnPlan {
     int32_t HG, HS, tile, lead, grid, threads, stages;
     size_t smem;
 };
+// fp32 rows (paged_attn_f32.cu).
+AttnPlan plan_f32(const lsa_page_cache &c, int Hq);
+lsa_status launch_f32(const AttnArgs &a, const AttnPlan &p, int grid, cudaStream_t st);
 // bf16 and e4m3 rows: the tensor-core kernel (paged_attn_mma.cu).
 AttnPlan plan_mma(const lsa_page_cache &c, int Hq);
 lsa_status launch_mma(const lsa_page_cache &c, const AttnArgs &a, const AttnPlan &p, int grid, cudaStream_t st);
