@@ -35,20 +35,25 @@ __global__ void __launch_bounds__(kCombineThreads) paged_attn_combine(AttnArgs a
     }
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float M = -INFINITY;
-    for (int p = threadIdx.x; p < P; p += kCombineThreads) M = fmaxf(M, a.part_ml[slot(p) * 2]);
+    auto ml = [&](int p) { return reinterpret_cast<const float2 *>(a.part_ml)[slot(p)]; };
+    // (m, l) of the thread's first partial stays in registers; few segments have more than 256
+    const float2 mine = threadIdx.x < P ? ml(threadIdx.x) : make_float2(-INFINITY, 0.f);
+    float M = mine.x;
+    for (int p = threadIdx.x + kCombineThreads; p < P; p += kCombineThreads) M = fmaxf(M, ml(p).x);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
     if (lane == 0) red[0][warp] = M;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kCombineThreads / 32; ++w) M = fmaxf(M, red[0][w]);
-    const float ref = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
-    for (int p = threadIdx.x; p < P; p += kCombineThreads) {
-        const float f = exp2f(a.part_ml[slot(p) * 2] - ref);
+    const float ref = M == -INFINITY ? 0.f : M, f0 = exp2_approx(mine.x - ref);
+    float L = f0 * mine.y;
+    if (threadIdx.x < P) wgt[threadIdx.x] = f0;
+    for (int p = threadIdx.x + kCombineThreads; p < P; p += kCombineThreads) {
+        const float2 x = ml(p);
+        const float f = exp2_approx(x.x - ref);
         wgt[p] = f;
-        L = fmaf(f, a.part_ml[slot(p) * 2 + 1], L);
+        L = fmaf(f, x.y, L);
     }
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
@@ -79,12 +84,9 @@ __global__ void __launch_bounds__(kCombineThreads) paged_attn_combine(AttnArgs a
     if (threadIdx.x < lanes) {
         for (int i = 1; i < groups; ++i) add(1.f, sums[i * lanes + lane4]);
         const float r = L == 0.f ? 0.f : 1.f / L;
-        store_out(a, hq * D + 4 * lane4, v.x * r);
-        store_out(a, hq * D + 4 * lane4 + 1, v.y * r);
-        store_out(a, hq * D + 4 * lane4 + 2, v.z * r);
-        store_out(a, hq * D + 4 * lane4 + 3, v.w * r);
+        store_out4(a, hq * D + 4 * lane4, make_float4(v.x * r, v.y * r, v.z * r, v.w * r));
     }
-    if (threadIdx.x == 0 && a.lse) a.lse[hq] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+    if (threadIdx.x == 0 && a.lse) a.lse[hq] = lse_of(M, L);
 }
 
 AttnPlan plan_of(const lsa_page_cache &c, int Hq) {

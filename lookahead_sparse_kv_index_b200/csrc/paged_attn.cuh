@@ -72,6 +72,13 @@ __device__ __forceinline__ int32_t units_of(const AttnArgs &a, int b) {
     return n ? n + a.lead : 0;
 }
 
+// a / b for a, b >= 0.  Unit counts fit 32 bits in all but the largest calls, and a 64-bit division is a hundred
+// instructions that every CTA would fetch before its first load.
+__device__ __noinline__ inline int64_t div64(int64_t a, int64_t b) { return a / b; }
+__device__ __forceinline__ int64_t div_units(int64_t a, int64_t b) {
+    return uint64_t(a | b) >> 32 ? div64(a, b) : int64_t(uint32_t(a) / uint32_t(b));
+}
+
 // Where a unit lies: sequence b, whose first unit is `base`.
 struct Where {
     int64_t total, share;   // units of the call, units of a CTA
@@ -104,7 +111,7 @@ __device__ inline Where find_start(const AttnArgs &a, int64_t cta, int64_t ctas,
     const int64_t heads = int64_t(a.cache.Hkv) * a.HG;
     Where r;
     r.total = total * heads;
-    r.share = (r.total + ctas - 1) / ctas;
+    r.share = div_units(r.total + ctas - 1, ctas);
     const int64_t start = cta * r.share;
     int64_t pre = before + inc - mine;
     if (start >= pre * heads && start < (pre + mine) * heads) {
@@ -146,6 +153,25 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
+__device__ __forceinline__ float log2_approx(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// log sum_t exp(a_t) from a softmax's reference m and sum L, both for 2^x.  lg2.approx is within 2^-22 of a value near 0
+// and of a part of 2^-22 of the others, below an fp32 lse's own step.
+__device__ __forceinline__ float lse_of(float m, float L) { return L == 0.f ? -INFINITY : (m + log2_approx(L)) * kLn2; }
+
+// Four consecutive elements of the output.
+__device__ __forceinline__ void store_out4(const AttnArgs &a, int64_t i, const float4 &v) {
+    if (a.q_f32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + i) = v;
+    } else {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + i) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+    }
+}
 __device__ __forceinline__ void store_out(const AttnArgs &a, int64_t i, float v) {
     if (a.q_f32) static_cast<float *>(a.out)[i] = v;
     else static_cast<__nv_bfloat16 *>(a.out)[i] = __float2bfloat16_rn(v);
@@ -186,14 +212,14 @@ __device__ __forceinline__ void for_pieces(const AttnArgs &a, int cta, int ctas,
             ++b;
             continue;
         }
-        const int hseg = int((u - base) / units), at = int((u - base) - int64_t(hseg) * units);
+        const int hseg = int(div_units(u - base, units)), at = int((u - base) - int64_t(hseg) * units);
         const int take = int(end - u < units - at ? end - u : units - at);
         const int t0 = max(at - a.lead, 0), t1 = max(at + take - a.lead, 0);
         if (t1 > t0) {
             const int lo = s.lo + t0 * a.tile, hi = t1 == n ? s.hi : s.lo + t1 * a.tile;
             if (t0 == 0 && threadIdx.x == 0 && (t1 < n || a.by_segment))
                 a.records[a.by_segment ? b * heads + hseg : cta] =
-                    Record{t1 < n ? b : -1, hseg, cta, int32_t((u - at + units - 1) / w.share)};
+                    Record{t1 < n ? b : -1, hseg, cta, int32_t(div_units(u - at + units - 1, w.share))};
             f(b, hseg, lo, hi, t0 == 0 && t1 == n ? -1 : 2 * cta + (t0 == 0));
         }
         u += take;
@@ -204,29 +230,33 @@ __device__ __forceinline__ void for_pieces(const AttnArgs &a, int cta, int ctas,
 // and writes the segment's output or the piece's partial.
 __device__ __forceinline__ void finish_piece(const AttnArgs &a, int b, int hseg, int slot, int n, const float *o,
                                              const float *ml) {
-    const int D = a.cache.D, HS = a.HS;
+    const int quads = a.cache.D / 4, HS = a.HS;
     const int first = (hseg % a.HG) * HS, heads = min(HS, a.G - first);
     const int64_t hq = int64_t(b) * a.Hq + (hseg / a.HG) * a.G + first;
-    for (int i = threadIdx.x; i < heads * D; i += blockDim.x) {
-        const int h = i / D, d = i - h * D;
+    for (int i = threadIdx.x; i < heads * quads; i += blockDim.x) {
+        const int h = i / quads, d = i - h * quads;
         float M = -INFINITY;
         for (int p = 0; p < n; ++p) M = fmaxf(M, ml[(p * HS + h) * 2]);
         const float ref = M == -INFINITY ? 0.f : M;
-        float L = 0.f, v = 0.f;
+        float L = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
         for (int p = 0; p < n; ++p) {
-            const float w = exp2f(ml[(p * HS + h) * 2] - ref);
-            L += w * ml[(p * HS + h) * 2 + 1];
-            v += w * o[(int64_t(p) * HS + h) * D + d];
+            const float w = exp2_approx(ml[(p * HS + h) * 2] - ref);
+            const float4 x = reinterpret_cast<const float4 *>(o)[(p * HS + h) * quads + d];
+            L = fmaf(w, ml[(p * HS + h) * 2 + 1], L);
+            v.x = fmaf(w, x.x, v.x);
+            v.y = fmaf(w, x.y, v.y);
+            v.z = fmaf(w, x.z, v.z);
+            v.w = fmaf(w, x.w, v.w);
         }
         if (slot < 0) {
-            store_out(a, (hq + h) * D + d, L == 0.f ? 0.f : v / L);
-            if (d == 0 && a.lse) a.lse[hq + h] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+            const float r = L == 0.f ? 0.f : 1.f / L;
+            store_out4(a, ((hq + h) * quads + d) * 4, make_float4(v.x * r, v.y * r, v.z * r, v.w * r));
+            if (d == 0 && a.lse) a.lse[hq + h] = lse_of(M, L);
         } else {
-            a.part_o[(int64_t(slot) * HS + h) * D + d] = v;
-            if (d == 0) {
-                a.part_ml[(int64_t(slot) * HS + h) * 2] = M;
-                a.part_ml[(int64_t(slot) * HS + h) * 2 + 1] = L;
-            }
+            reinterpret_cast<float4 *>(a.part_o)[(int64_t(slot) * HS + h) * quads + d] = v;
+            if (d == 0) reinterpret_cast<float2 *>(a.part_ml)[int64_t(slot) * HS + h] = make_float2(M, L);
         }
     }
 }

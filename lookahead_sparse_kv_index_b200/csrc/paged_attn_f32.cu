@@ -16,7 +16,7 @@ namespace lsa {
 namespace paged {
 namespace {
 
-constexpr int kMaxWarps = 4;
+constexpr int kMaxWarps = 4, kMaxStages = 4;
 constexpr float kLag = 8.f;
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return uint32_t(__cvta_generic_to_shared(p)); }
@@ -109,14 +109,21 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_f32(AttnArgs a, int
             cp_commit();
         };
 
-        int64_t ahead = locate();
-        for (int j = 0; j < stages - 1; ++j) {
-            issue(j, j, ahead);
-            ahead = locate();
-        }
+        // the loads that the first stages wait for are all on their way before any is waited for: q, then the pages
         const float *q = reinterpret_cast<const float *>(static_cast<const uint8_t *>(a.q) + int64_t(b) * a.q_stride) +
                          (int64_t(kvh) * a.G + first) * D;
-        for (int i = threadIdx.x; i < NH * D; i += blockDim.x) qs[i] = first + i / D < a.G ? q[i] : 0.f;
+        for (int i = threadIdx.x; i < NH * nch; i += blockDim.x)
+            cp_async16(smem_addr(qs) + i * 16, q + i * 4, first + i / nch < a.G);
+        int64_t early[kMaxStages - 1];
+#pragma unroll
+        for (int j = 0; j < kMaxStages - 1; ++j)
+            if (j < stages - 1) early[j] = locate();
+        int64_t ahead = locate();
+#pragma unroll
+        for (int j = 0; j < kMaxStages - 1; ++j)
+            if (j < stages - 1) issue(j, j, early[j]);      // (q is in the first group)
+        // (a warp's first wait does not cover the q of other warps)
+        cp_wait(stages - 2);
         __syncthreads();
 
         float m[NH], l[NH], o[NH][KC][4];
@@ -257,7 +264,7 @@ struct Run {
         p.HG = (G + NH - 1) / NH;
         // two CTAs of four warps on an SM: up to three stages a warp
         int stages = (112 * 1024 - q) / (kMaxWarps * stage);
-        p.stages = stages > 4 ? 4 : stages < 2 ? 2 : stages;
+        p.stages = stages > kMaxStages ? kMaxStages : stages < 2 ? 2 : stages;
         p.threads = kMaxWarps * 32;
         p.tile = C::kStage * kMaxWarps;
         p.lead = 6;

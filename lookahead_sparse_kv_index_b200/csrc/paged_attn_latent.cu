@@ -528,7 +528,7 @@ paged_attn_latent(AttnArgs a) {
                         a.part_ml[(int64_t(slot) * kHeads + head) * 2] = m;
                         a.part_ml[(int64_t(slot) * kHeads + head) * 2 + 1] = L;
                     } else if (a.lse) {
-                        a.lse[hq + head] = L == 0.f ? -INFINITY : (m + log2f(L)) * kLn2;
+                        a.lse[hq + head] = lse_of(m, L);
                     }
                 }
             }

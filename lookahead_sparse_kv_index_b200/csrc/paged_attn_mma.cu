@@ -138,7 +138,7 @@ struct Shape {
     __host__ __device__ static constexpr int stage(bool latent) { return kRows * (latent ? 1 : 2) + kTail; }
 };
 
-constexpr int kMaxWarps = 4;
+constexpr int kMaxWarps = 4, kMaxStages = 4;
 constexpr float kLag = 8.f;
 
 template <bool E4M3, int KB, int NT>
@@ -225,11 +225,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int
             cp_commit();
         };
 
+        // the pages of the first stages are all on their way before any is waited for
+        Entry early[kMaxStages - 1];
+#pragma unroll
+        for (int j = 0; j < kMaxStages - 1; ++j)
+            if (j < stages - 1) early[j] = locate();
         Entry ahead = locate();
-        for (int j = 0; j < stages - 1; ++j) {
-            issue(j, j, ahead);
-            ahead = locate();
-        }
 
         // q fragments of the piece's heads: lane (g, c) of block kb and head group nt holds head 8 nt + g, piece 4 kb + c
         {
@@ -254,30 +255,34 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int
                 const int l = i & 31, nt = (i >> 5) % NT, kb = (i >> 5) / NT;
                 const int h = nt * 8 + (l >> 2), p = kb * 4 + (l & 3);
                 const bool ok = first + h < a.G && p < nch;
-                uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-                if (ok) {
-#pragma unroll
-                    for (int x = 0; x < C::kQPer; ++x)
-                        v[x] = *reinterpret_cast<const uint4 *>(q + int64_t(h) * D + p * C::kElems + 8 * x);
-                }
-                if constexpr (E4M3) {
+                const uint16_t *from = q + int64_t(h) * D + p * C::kElems;
+                const uint32_t to = qf + ((kb * NT + nt) * C::kQPer) * 512 + l * 16;
+                if constexpr (!E4M3) {
+                    cp_async16(to, from, ok);
+                } else {
                     const float f = q_scale[h];
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        uint32_t *w = reinterpret_cast<uint32_t *>(&v[x]);
+                        const uint4 v = ok ? reinterpret_cast<const uint4 *>(from)[x] : make_uint4(0, 0, 0, 0);
+                        uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {
                             const __half2 t = __floats2half2_rn(__uint_as_float(w[y] << 16) * f,
                                                                 __uint_as_float(w[y] & 0xffff0000u) * f);
                             w[y] = *reinterpret_cast<const uint32_t *>(&t);
                         }
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + x * 512), "r"(w[0]), "r"(w[1]),
+                                     "r"(w[2]), "r"(w[3])
+                                     : "memory");
                     }
                 }
-#pragma unroll
-                for (int x = 0; x < C::kQPer; ++x)
-                    *reinterpret_cast<uint4 *>(smem + ((size_t(kb) * NT + nt) * C::kQPer + x) * 512 + l * 16) = v[x];
             }
         }
+#pragma unroll
+        for (int j = 0; j < kMaxStages - 1; ++j)
+            if (j < stages - 1) issue(j, j, early[j]);      // (q is in the first group)
+        // (a warp's first wait does not cover the q of other warps)
+        if constexpr (!E4M3) cp_wait(stages - 2);
         __syncthreads();
         uint4 qr[C::kQInRegs ? KB * NT * C::kQPer : 1];
         if constexpr (C::kQInRegs) {
@@ -559,7 +564,7 @@ struct Run {
                 stages = fit(222 * 1024);
             }
         }
-        p.stages = stages > 4 ? 4 : stages;
+        p.stages = stages > kMaxStages ? kMaxStages : stages;
         p.threads = warps * 32;
         p.tile = C::kStep * warps;
         p.lead = 6;
