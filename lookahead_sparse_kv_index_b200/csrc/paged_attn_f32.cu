@@ -267,7 +267,7 @@ struct Run {
         p.stages = stages > kMaxStages ? kMaxStages : stages < 2 ? 2 : stages;
         p.threads = kMaxWarps * 32;
         p.tile = C::kStage * kMaxWarps;
-        p.lead = 6;
+        p.lead = 3;
         p.grid = sm_count() * 2;
         const size_t ring = size_t(p.stages) * kMaxWarps * stage, join = size_t(kMaxWarps) * NH * (D + 2) * 4;
         p.smem = q + (ring > join ? ring : join);

@@ -19,8 +19,9 @@
 // its own head, which is exact for elements down to 2^-28 of the head's largest and off by less than 2^-38 of it below;
 // the scales of K multiply the fp32 scores, those of V the weights before they are rounded, relative to the largest
 // scale 2^R so far (o is rescaled when R grows, as it is when the running max does).
-// A weight is rounded to 16 bits for its product with V and the rest rounded again, so it enters as a sum of two 16-bit
-// numbers (within 2^-17 for bf16): with one, its rounding is as large as the output's own and showed in the result.
+// Weights.  A bf16 weight's rounding (2^-9) is as large as the output's own, and with one such number a weight the error
+// of the result is 1.4 times that of rounding it once; so what the rounding left is rounded too and multiplied as well
+// (2^-17 then).  An f16 weight's rounding (2^-12) is an eighth of the output's: one number does.
 #include <limits.h>
 
 #include "paged_attn.cuh"
@@ -87,22 +88,17 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// Two weights as 16-bit numbers, and what their rounding left as two more.
-template <bool F16>
-__device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &lo) {
-    if constexpr (F16) {
-        const __half2 h = __floats2half2_rn(x, y);
-        const float2 f = __half22float2(h);
-        const __half2 r = __floats2half2_rn(x - f.x, y - f.y);
-        hi = *reinterpret_cast<const uint32_t *>(&h);
-        lo = *reinterpret_cast<const uint32_t *>(&r);
-    } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-        const float2 f = __bfloat1622float2(h);
-        const __nv_bfloat162 r = __floats2bfloat162_rn(x - f.x, y - f.y);
-        hi = *reinterpret_cast<const uint32_t *>(&h);
-        lo = *reinterpret_cast<const uint32_t *>(&r);
-    }
+// Two weights as bf16 numbers, and what their rounding left as two more.
+__device__ __forceinline__ void split_bf16(float x, float y, uint32_t &hi, uint32_t &lo) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    const float2 f = __bfloat1622float2(h);
+    const __nv_bfloat162 r = __floats2bfloat162_rn(x - f.x, y - f.y);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t pack_f16(float x, float y) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&h);
 }
 
 // Staged row of fragment index r (0 .. 15), chosen so that no read of shared memory has bank conflicts while rows are an
@@ -434,22 +430,25 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) ref[nt][x] = m[nt][x] == -INFINITY ? 0.f : m[nt][x];
-            uint32_t ph[C::kM][NT][2], pl[C::kM][NT][2];
+            uint32_t ph[C::kM][NT][2], pl[C::kM][NT][2];    // (pl: bf16 rows alone)
 #pragma unroll
             for (int tm = 0; tm < C::kM; ++tm)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        float p0 = exp2_approx(s[tm][nt][2 * y] - ref[nt][0]);
-                        float p1 = exp2_approx(s[tm][nt][2 * y + 1] - ref[nt][1]);
+                        const float p0 = exp2_approx(s[tm][nt][2 * y] - ref[nt][0]);
+                        const float p1 = exp2_approx(s[tm][nt][2 * y + 1] - ref[nt][1]);
                         l[nt][0] += p0;
                         l[nt][1] += p1;
-                        if constexpr (E4M3) p0 *= vs[tm][y], p1 *= vs[tm][y];
-                        uint32_t h, r;
-                        split<E4M3>(p0, p1, h, r);
-                        ph[tm][nt][y] = movmatrix(h);
-                        pl[tm][nt][y] = movmatrix(r);
+                        if constexpr (E4M3) {
+                            ph[tm][nt][y] = movmatrix(pack_f16(p0 * vs[tm][y], p1 * vs[tm][y]));
+                        } else {
+                            uint32_t h, r;
+                            split_bf16(p0, p1, h, r);
+                            ph[tm][nt][y] = movmatrix(h);
+                            pl[tm][nt][y] = movmatrix(r);
+                        }
                     }
             if constexpr (E4M3) {
 #pragma unroll
@@ -478,7 +477,6 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int
                                 for (int nt = 0; nt < NT; ++nt) {
                                     float(&d)[4] = o[p * 8 + 2 * i + y][nt];
                                     mma<true>(d, a0, a1, a2, a3, ph[tm][nt][0], ph[tm][nt][1]);
-                                    mma<true>(d, a0, a1, a2, a3, pl[tm][nt][0], pl[tm][nt][1]);
                                 }
                             }
                         }
@@ -567,7 +565,7 @@ struct Run {
         p.stages = stages > kMaxStages ? kMaxStages : stages;
         p.threads = warps * 32;
         p.tile = C::kStep * warps;
-        p.lead = 6;
+        p.lead = 3;
         p.grid = sm_count() * ctas;
         const size_t ring = size_t(p.stages) * warps * stage, join = size_t(warps) * C::kHeads * (D + 2) * 4;
         p.smem = C::kQBytes + (ring > join ? ring : join);
