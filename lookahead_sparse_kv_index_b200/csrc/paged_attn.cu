@@ -24,8 +24,8 @@ __global__ void __launch_bounds__(kCombineThreads) paged_attn_combine(AttnArgs a
     const Record rec = a.records[blockIdx.x];
     const int in = (rec.hseg % a.HG) * HS + h;
     if (rec.b < 0 || in >= a.G) return;
-    const int c = rec.first, P = rec.last - c + 1;
-    auto slot = [&](int p) { return int64_t(p == 0 ? 2 * c + 1 : 2 * (c + p)) * HS + h; };
+    const int c = rec.first, P = (rec.last - c) / a.lanes + 1;
+    auto slot = [&](int p) { return int64_t(p == 0 ? 2 * c + 1 : 2 * (c + p * a.lanes)) * HS + h; };
     const int lanes = D / 4, groups = kCombineThreads / lanes, lane4 = threadIdx.x % lanes, grp = threadIdx.x / lanes;
     float4 ahead[kAhead];
 #pragma unroll
@@ -223,6 +223,8 @@ extern "C" lsa_status lsa_paged_attn(const void *Q, lsa_dtype q_dtype, int64_t q
     a.whole = most <= int64_t(kWholeUnits) * p.tile && segments < (int64_t(1) << 31);
     const int grid = a.whole ? int(segments) : p.grid;
     a.by_segment = segments <= grid;
+    const int heads = cache->Hkv * p.HG;
+    a.lanes = heads <= grid && grid % heads * 16 <= grid ? heads : 1;      // at most a sixteenth of the CTAs stays idle
     cudaStream_t st = as_stream(stream);
     s = cache->dtype == LSA_F32 ? launch_f32(a, p, grid, st)
         : latent_supported(*cache, Hq) ? launch_latent(a, grid, st) : launch_mma(*cache, a, p, grid, st);

@@ -9,6 +9,9 @@
 // there; of the others each CTA writes a partial (unnormalised o, and the running max m and sum l of its softmax, both
 // for 2^x), and the combine kernel joins a segment's partials in unit order:
 //     M = max m_c,  L = sum l_c 2^(m_c - M),  o = sum o_c 2^(m_c - M) / L,  lse = (M + log2 L) ln 2.
+// Where the heads divide the grid well enough, the CTAs are split among them first: CTA c does head group c % heads of
+// the units (of sequences alone, then) of run c / heads, so that neighbours read neighbouring heads of the same entries
+// at the same time and HBM sees whole lines of the cache rather than one head's 128 bytes of each.
 // A CTA has at most two partials: slot 2c for the piece that continues a segment, 2c + 1 for one that begins it; where
 // it begins one, it records which, and the record's combine CTAs join it.  There is a record for each CTA, or for each
 // segment where these are fewer.
@@ -41,6 +44,7 @@ struct AttnArgs {
     float *part_o, *part_ml;     // [2 * grid][HS][D], [2 * grid][HS][2]
     Record *records;             // [grid], or [segments]
     int32_t by_segment;
+    int32_t lanes;               // head groups that the CTAs are split among (1: units run through them)
     int32_t *err;
     int32_t tile, lead;
     int32_t whole;               // 1: CTA c does segment c and no partials are written
@@ -87,7 +91,7 @@ struct Where {
 };
 
 // Finds where the first unit of CTA `cta` of `ctas` lies (whole block; `scratch`: 40 int64 of shared memory).
-__device__ inline Where find_start(const AttnArgs &a, int64_t cta, int64_t ctas, int64_t *scratch) {
+__device__ inline Where find_start(const AttnArgs &a, int64_t cta, int64_t ctas, int heads_of_unit, int64_t *scratch) {
     const int threads = blockDim.x, warps = threads >> 5;
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int per = (a.B + threads - 1) / threads;
@@ -108,7 +112,7 @@ __device__ inline Where find_start(const AttnArgs &a, int64_t cta, int64_t ctas,
         if (w < warp) before += scratch[w];
         total += scratch[w];
     }
-    const int64_t heads = int64_t(a.cache.Hkv) * a.HG;
+    const int64_t heads = heads_of_unit;
     Where r;
     r.total = total * heads;
     r.share = div_units(r.total + ctas - 1, ctas);
@@ -199,27 +203,29 @@ __device__ __forceinline__ void for_pieces(const AttnArgs &a, int cta, int ctas,
         if (a.lse)
             for (int i = threadIdx.x; i < a.Hq; i += blockDim.x) a.lse[int64_t(e) * a.Hq + i] = -INFINITY;
     }
-    const Where w = find_start(a, cta, ctas, scratch);
+    const int run = cta / a.lanes, own = cta - run * a.lanes, through = heads / a.lanes;   // (lanes is 1 or heads)
+    const Where w = find_start(a, run, ctas / a.lanes, through, scratch);
     if (w.b < 0) return;
     int b = w.b;
-    int64_t base = w.base, u = cta * w.share;
+    int64_t base = w.base, u = run * w.share;
     const int64_t end = u + w.share < w.total ? u + w.share : w.total;
     while (u < end) {
         const Seen s = seen_of(a, b);
         const int n = (s.hi - s.lo + a.tile - 1) / a.tile, units = n ? n + a.lead : 0;
-        if (u - base >= int64_t(units) * heads) {   // past this sequence
-            base += int64_t(units) * heads;
+        if (u - base >= int64_t(units) * through) {   // past this sequence
+            base += int64_t(units) * through;
             ++b;
             continue;
         }
-        const int hseg = int(div_units(u - base, units)), at = int((u - base) - int64_t(hseg) * units);
+        const int pass = int(div_units(u - base, units)), at = int((u - base) - int64_t(pass) * units);
+        const int hseg = own + pass;
         const int take = int(end - u < units - at ? end - u : units - at);
         const int t0 = max(at - a.lead, 0), t1 = max(at + take - a.lead, 0);
         if (t1 > t0) {
             const int lo = s.lo + t0 * a.tile, hi = t1 == n ? s.hi : s.lo + t1 * a.tile;
             if (t0 == 0 && threadIdx.x == 0 && (t1 < n || a.by_segment))
                 a.records[a.by_segment ? b * heads + hseg : cta] =
-                    Record{t1 < n ? b : -1, hseg, cta, int32_t(div_units(u - at + units - 1, w.share))};
+                    Record{t1 < n ? b : -1, hseg, cta, int32_t(div_units(u - at + units - 1, w.share)) * a.lanes + own};
             f(b, hseg, lo, hi, t0 == 0 && t1 == n ? -1 : 2 * cta + (t0 == 0));
         }
         u += take;
