@@ -25,28 +25,30 @@ struct Books {
     int64_t n_pages;
 };
 
-// Inclusive sum over the block of one value a thread; *total is the block's.  `part`: 33 ints of shared memory.
-__device__ __forceinline__ int block_scan(int v, int *part, int *total) {
+// Inclusive sum over the block of one value a thread; *total is the block's.  `part`: 33 values of shared memory, which
+// calls may use one after the other.
+template <typename V>
+__device__ __forceinline__ V block_scan(V v, V *part, V *total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int s = v;
+    V s = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, s, o);
+        const V up = __shfl_up_sync(0xffffffffu, s, o);
         if (lane >= o) s += up;
     }
     if (lane == 31) part[warp] = s;
     __syncthreads();
     if (warp == 0) {
-        int w = part[lane];
+        V w = part[lane];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int up = __shfl_up_sync(0xffffffffu, w, o);
+            const V up = __shfl_up_sync(0xffffffffu, w, o);
             if (lane >= o) w += up;
         }
         part[lane] = w;
     }
     __syncthreads();
-    const int before = warp ? part[warp - 1] : 0;
+    const V before = warp ? part[warp - 1] : 0;
     *total = part[31];
     __syncthreads();
     return before + s;
@@ -72,12 +74,13 @@ __device__ __forceinline__ uint32_t free_mask(const Books &bk, int64_t r) {
     return m;
 }
 
-// Whether the pool has `need` free pages (whole block).
-__device__ bool enough_free(const Books &bk, int64_t need, int *part) {
+// Whether the pool has `need` free pages (whole block).  `mask0`: round 0's free pages, which its caller asks for before
+// anything else; most calls end there.
+__device__ bool enough_free(const Books &bk, int64_t need, uint32_t mask0, int *part) {
     int64_t have = 0;
     for (int64_t r = 0; have < need && r * kRound < bk.n_pages; ++r) {
         int total;
-        block_scan(__popc(free_mask(bk, r)), part, &total);
+        block_scan(__popc(r ? free_mask(bk, r) : mask0), part, &total);
         have += total;
     }
     return have >= need;
@@ -86,10 +89,10 @@ __device__ bool enough_free(const Books &bk, int64_t need, int *part) {
 // Hands the `need` lowest free pages out (whole block): give(k, page) for the k-th, by one thread.  give may write the
 // page's own count.
 template <typename F>
-__device__ void hand_out(const Books &bk, int64_t need, int *part, F give) {
+__device__ void hand_out(const Books &bk, int64_t need, uint32_t mask0, int *part, F give) {
     int64_t given = 0;
     for (int64_t r = 0; given < need && r * kRound < bk.n_pages; ++r) {
-        uint32_t m = free_mask(bk, r);
+        uint32_t m = r ? free_mask(bk, r) : mask0;
         int total;
         int64_t k = given + block_scan(__popc(m), part, &total) - __popc(m);
         for (; m && k < need; ++k) {
@@ -101,25 +104,22 @@ __device__ void hand_out(const Books &bk, int64_t need, int *part, F give) {
     }
 }
 
-__device__ __forceinline__ int64_t held_entries(const Books &bk, int r) {
+// Entries that row r holds, and the pages of n entries (both below 2^31).
+__device__ __forceinline__ uint32_t held_entries(const Books &bk, int r) {
     const int64_t n = bk.len[r], reach = int64_t(bk.max_pages) * bk.page_size;
-    return n < 0 ? 0 : n > reach ? reach : n;
+    return uint32_t(n < 0 ? 0 : n > reach ? reach : n);
 }
-__device__ __forceinline__ int64_t pages_of(const Books &bk, int64_t n) { return (n + bk.page_size - 1) / bk.page_size; }
+__device__ __forceinline__ uint32_t pages_of(const Books &bk, uint32_t n) {
+    return (n + uint32_t(bk.page_size) - 1) / uint32_t(bk.page_size);
+}
 
-// 64-bit prefix over the block of what each thread's items need; `first` [kBooks + 1] in shared memory.
-__device__ __forceinline__ int64_t prefix64(int64_t mine, int64_t *first) {
-    // two 32-bit scans would do; a shared-memory doubling scan is simple and runs once a call
-    first[threadIdx.x + 1] = mine;
+// What the threads' items need, summed up to each thread: first[t] in shared memory, the sum is returned.
+__device__ __forceinline__ int64_t prefix(int64_t mine, int64_t *first, int64_t *part) {
+    int64_t total;
+    first[threadIdx.x + 1] = block_scan(mine, part, &total);
     if (threadIdx.x == 0) first[0] = 0;
     __syncthreads();
-    for (int o = 1; o < kBooks; o <<= 1) {
-        const int64_t up = int(threadIdx.x) >= o ? first[threadIdx.x + 1 - o] : 0;
-        __syncthreads();
-        first[threadIdx.x + 1] += up;
-        __syncthreads();
-    }
-    return first[kBooks];
+    return total;
 }
 
 // The thread whose items hold the k-th page: first[t] <= k < first[t + 1].
@@ -133,35 +133,38 @@ __device__ __forceinline__ int thread_of(const int64_t *first, int64_t k) {
 }
 
 __global__ void __launch_bounds__(kBooks) page_grow(Books bk, const int32_t *__restrict__ add, int32_t *err) {
-    __shared__ int64_t first[kBooks + 1];
+    __shared__ int64_t first[kBooks + 1], part64[33];
     __shared__ int part[33];
     pdl_launch_dependents();
     pdl_wait();
+    const uint32_t mask0 = free_mask(bk, 0);
     const int per = (bk.n_rows + kBooks - 1) / kBooks;
     const int r0 = min(bk.n_rows, int(threadIdx.x) * per), r1 = min(bk.n_rows, r0 + per);
     const int64_t reach = int64_t(bk.max_pages) * bk.page_size;
-    auto need_of = [&](int r, int64_t *have) {
-        const int64_t n = held_entries(bk, r), more = add[r] > 0 ? add[r] : 0;
+    // pages that row r holds and pages that it needs besides (more than it may have counts as past the end)
+    auto need_of = [&](int r, uint32_t *have, bool *past) {
+        const uint32_t n = held_entries(bk, r), more = add[r] > 0 ? add[r] : 0;
+        *past |= int64_t(n) + more > reach;
         *have = pages_of(bk, n);
-        return pages_of(bk, n + more) - *have;
+        return *past ? 0u : pages_of(bk, n + more) - *have;
     };
-    int64_t need = 0, have;
+    int64_t need = 0;
+    uint32_t have;
     bool past = false;
-    for (int r = r0; r < r1; ++r) {
-        need += need_of(r, &have);
-        past |= held_entries(bk, r) + (add[r] > 0 ? add[r] : 0) > reach;
-    }
+    for (int r = r0; r < r1; ++r) need += need_of(r, &have, &past);
     past = __syncthreads_or(past);
-    const int64_t total = prefix64(need, first);
-    if (past || !enough_free(bk, total, part)) {
+    const int64_t total = prefix(need, first, part64);
+    if (past || !enough_free(bk, total, mask0, part)) {
         if (threadIdx.x == 0) raise_err(err, LSA_ERR_CAPACITY);
         return;
     }
-    hand_out(bk, total, part, [&](int64_t k, int32_t page) {
+    hand_out(bk, total, mask0, part, [&](int64_t k, int32_t page) {
         const int t = thread_of(first, k);
-        int64_t at = first[t], have;
+        int64_t at = first[t];
+        uint32_t have;
+        bool past = false;
         for (int r = t * per;; ++r) {
-            const int64_t n = need_of(r, &have);
+            const uint32_t n = need_of(r, &have, &past);
             if (k < at + n) {
                 bk.table[int64_t(r) * bk.max_pages + have + (k - at)] = page;
                 bk.refs[page] = 1;
@@ -180,22 +183,25 @@ __global__ void __launch_bounds__(kBooks) page_grow(Books bk, const int32_t *__r
 __global__ void __launch_bounds__(kBooks) page_fork_take(Books bk, const int32_t *__restrict__ src,
                                                          const int32_t *__restrict__ dst, int n, int32_t *copy_src,
                                                          int32_t *copy_dst, int32_t *err) {
-    __shared__ int64_t first[kBooks + 1];
+    __shared__ int64_t first[kBooks + 1], part64[33];
     __shared__ int part[33];
     __shared__ uint32_t named[kMaxRows / 32];
     pdl_launch_dependents();
     pdl_wait();
-    for (int i = threadIdx.x; i < kMaxRows / 32; i += kBooks) named[i] = 0;
-    __syncthreads();
+    const uint32_t mask0 = free_mask(bk, 0);
     const int per = (n + kBooks - 1) / kBooks;
     const int i0 = min(n, int(threadIdx.x) * per), i1 = min(n, i0 + per);
-    auto part_filled = [&](int i) { return held_entries(bk, src[i]) % bk.page_size > 0; };
+    auto part_filled = [&](int i) { return held_entries(bk, src[i]) % uint32_t(bk.page_size) > 0; };
+    for (int i = threadIdx.x; i < (bk.n_rows + 31) / 32; i += kBooks) named[i] = 0;
+    __syncthreads();
     bool bad = false;
+    int64_t need = 0;
     for (int i = i0; i < i1; ++i) {
         const int s = src[i], d = dst[i];
         if (s < 0 || s >= bk.n_rows || d < 0 || d >= bk.n_rows) {
             bad = true;
         } else {
+            need += part_filled(i);
             bad |= bk.len[d] != 0;
             bad |= (atomicOr(&named[d >> 5], 1u << (d & 31)) >> (d & 31)) & 1u;
         }
@@ -204,11 +210,8 @@ __global__ void __launch_bounds__(kBooks) page_fork_take(Books bk, const int32_t
     if (!bad)      // a row that becomes a copy cannot be copied in the same call
         for (int i = i0; i < i1; ++i) bad |= (named[src[i] >> 5] >> (src[i] & 31)) & 1u;
     bad = __syncthreads_or(bad);
-    int64_t need = 0;
-    if (!bad)
-        for (int i = i0; i < i1; ++i) need += part_filled(i);
-    const int64_t total = prefix64(need, first);
-    if (bad || !enough_free(bk, total, part)) {
+    const int64_t total = prefix(need, first, part64);
+    if (bad || !enough_free(bk, total, mask0, part)) {
         if (threadIdx.x == 0) raise_err(err, bad ? LSA_ERR_INVALID : LSA_ERR_CAPACITY);
         for (int i = threadIdx.x; i < n; i += kBooks) {
             copy_src[i] = -2;
@@ -219,13 +222,13 @@ __global__ void __launch_bounds__(kBooks) page_fork_take(Books bk, const int32_t
     for (int i = i0; i < i1; ++i) {
         if (!part_filled(i)) copy_src[i] = copy_dst[i] = -1;
     }
-    hand_out(bk, total, part, [&](int64_t k, int32_t page) {
+    hand_out(bk, total, mask0, part, [&](int64_t k, int32_t page) {
         const int t = thread_of(first, k);
         int64_t at = first[t];
         for (int i = t * per;; ++i) {
             const bool one = part_filled(i);
             if (one && k == at) {
-                const int64_t full = held_entries(bk, src[i]) / bk.page_size;
+                const uint32_t full = held_entries(bk, src[i]) / uint32_t(bk.page_size);
                 const int32_t from = bk.table[int64_t(src[i]) * bk.max_pages + full];
                 bk.table[int64_t(dst[i]) * bk.max_pages + full] = page;
                 bk.refs[page] = 1;
@@ -252,8 +255,9 @@ __global__ void __launch_bounds__(kFork) page_fork_share(Books bk, const int32_t
         if (threadIdx.x == 0) copy_src[i] = -1;
         return;
     }
-    const int64_t s = src[i], d = dst[i], n = held_entries(bk, int(s));
-    const int64_t full = n / bk.page_size, held = pages_of(bk, n);
+    const int64_t s = src[i], d = dst[i];
+    const uint32_t n = held_entries(bk, int(s));
+    const int64_t full = n / uint32_t(bk.page_size), held = pages_of(bk, n);
     for (int64_t c = threadIdx.x; c < bk.max_pages; c += kFork) {
         if (c < full) {
             const int32_t page = bk.table[s * bk.max_pages + c];
@@ -278,7 +282,7 @@ __global__ void __launch_bounds__(kFork) page_free(Books bk, const int32_t *__re
     }
     if (threadIdx.x == 0) {
         const int64_t n = atomicExch(&bk.len[r], 0), reach = int64_t(bk.max_pages) * bk.page_size;
-        held_s = int(pages_of(bk, n < 0 ? 0 : n > reach ? reach : n));
+        held_s = int(pages_of(bk, uint32_t(n < 0 ? 0 : n > reach ? reach : n)));
     }
     __syncthreads();
     const int held = held_s;
@@ -302,9 +306,13 @@ constexpr int kPack = 1024, kPackPages = kPack * 4;
 
 __device__ __forceinline__ int held_of4(const Books &bk, int64_t p0, uint32_t *mask) {
     uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (p0 + i < bk.n_pages && bk.refs[p0 + i] > 0) m |= 1u << i;
+    if (p0 + 4 <= bk.n_pages && (reinterpret_cast<uintptr_t>(bk.refs) & 15) == 0) {
+        const int4 v = *reinterpret_cast<const int4 *>(bk.refs + p0);
+        m = uint32_t(v.x > 0) | uint32_t(v.y > 0) << 1 | uint32_t(v.z > 0) << 2 | uint32_t(v.w > 0) << 3;
+    } else {
+        for (int i = 0; i < 4; ++i)
+            if (p0 + i < bk.n_pages && bk.refs[p0 + i] > 0) m |= 1u << i;
+    }
     *mask = m;
     return __popc(m);
 }
@@ -319,39 +327,63 @@ __global__ void __launch_bounds__(kPack) pack_count(Books bk, int32_t *cnt) {
     if (threadIdx.x == 0) cnt[blockIdx.x] = total;
 }
 
+// Three sums over the block at once (whole block; `part`: [3][32] of shared memory).
+__device__ __forceinline__ void block_sum3(int (&v)[3], int (*part)[32]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        v[i] = __reduce_add_sync(0xffffffffu, v[i]);
+        if (lane == 0) part[i][warp] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 3; ++i) v[i] = __reduce_add_sync(0xffffffffu, part[i][lane]);
+    __syncthreads();
+}
+
+// kSmallPool: a pool of up to so many pages is counted by every block for itself, which takes less than a launch.
+constexpr int64_t kSmallPool = 16 * kPackPages;
+
 __global__ void __launch_bounds__(kPack) pack_moves(Books bk, const int32_t *__restrict__ cnt, int blocks,
                                                     int32_t *__restrict__ rank, int32_t *move_src, int32_t *move_dst,
                                                     int32_t *n_moves) {
-    __shared__ int part[33];
-    __shared__ int s_before, s_total;
+    __shared__ int part[33], part3[3][32];
     pdl_launch_dependents();
     pdl_wait();
-    if (threadIdx.x == 0) s_before = s_total = 0;
-    __syncthreads();
-    int before = 0, total = 0;
-    for (int i = threadIdx.x; i < blocks; i += kPack) {
-        total += cnt[i];
-        if (i < int(blockIdx.x)) before += cnt[i];
-    }
-    atomicAdd(&s_before, before);
-    atomicAdd(&s_total, total);
-    __syncthreads();
-    const int L = s_total, block_before = s_before;
-    // held(L): the blocks before L's, and the pages of its block below L
-    __shared__ int s_front;
-    if (threadIdx.x == 0) s_front = 0;
-    __syncthreads();
-    const int lb = L / kPackPages;
-    int front = 0;
-    for (int i = threadIdx.x; i < lb && i < blocks; i += kPack) front += cnt[i];
-    for (int64_t p = int64_t(lb) * kPackPages + threadIdx.x; p < L; p += kPack) front += bk.refs[p] > 0;
-    atomicAdd(&s_front, front);
-    __syncthreads();
-    const int held_front = s_front, M = L - held_front;
-
     const int64_t p0 = int64_t(blockIdx.x) * kPackPages + threadIdx.x * 4;
     uint32_t m;
-    int mine = held_of4(bk, p0, &m), all;
+    const int mine = held_of4(bk, p0, &m);
+    // all held pages, those of the blocks before this one
+    int sum[3] = {0, 0, 0};
+    if (bk.n_pages <= kSmallPool) {
+        for (int64_t p = threadIdx.x * 4; p < bk.n_pages; p += kPackPages) {
+            uint32_t any;
+            const int c = held_of4(bk, p, &any);
+            sum[0] += c;
+            if (p < int64_t(blockIdx.x) * kPackPages) sum[1] += c;
+        }
+    } else {
+        for (int i = threadIdx.x; i < blocks; i += kPack) {
+            sum[0] += cnt[i];
+            if (i < int(blockIdx.x)) sum[1] += cnt[i];
+        }
+    }
+    block_sum3(sum, part3);
+    const int L = sum[0], block_before = sum[1];
+    // held(L): with the counts at hand, the blocks before L's and the pages of its block below L
+    int front[3] = {0, 0, 0};
+    const int lb = bk.n_pages <= kSmallPool ? 0 : L / kPackPages;
+    for (int i = threadIdx.x; i < lb; i += kPack) front[0] += cnt[i];
+    for (int64_t p = int64_t(lb) * kPackPages + threadIdx.x * 4; p < L; p += kPackPages) {
+        uint32_t any;
+        held_of4(bk, p, &any);
+        if (p + 4 > L) any &= (1u << (L - p)) - 1u;
+        front[0] += __popc(any);
+    }
+    block_sum3(front, part3);
+    const int held_front = front[0], M = L - held_front;
+
+    int all;
     int held = block_before + block_scan(mine, part, &all) - mine;
     for (int i = 0; i < 4; ++i) {
         const int64_t p = p0 + i;
@@ -554,8 +586,10 @@ extern "C" lsa_status lsa_page_compact(const lsa_page_table *pt, int32_t *table_
     int32_t *cnt = static_cast<int32_t *>(workspace);
     int32_t *rank = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + align_up(size_t(blocks) * 4, 256));
     cudaStream_t st = as_stream(stream);
-    LSA_CUDA(launch_pdl(pack_count, dim3(blocks), dim3(kPack), 0, st, bk, cnt));
-    LSA_LAUNCHED("pack_count");
+    if (pt->n_pages > kSmallPool) {
+        LSA_CUDA(launch_pdl(pack_count, dim3(blocks), dim3(kPack), 0, st, bk, cnt));
+        LSA_LAUNCHED("pack_count");
+    }
     LSA_CUDA(launch_pdl(pack_moves, dim3(blocks), dim3(kPack), 0, st, bk, static_cast<const int32_t *>(cnt), blocks,
                         rank, move_src, move_dst, n_moves));
     LSA_LAUNCHED("pack_moves");

@@ -490,7 +490,8 @@ class Pool:
 
 
 @pytest.mark.parametrize("n_rows,max_pages,n_pages,page,seed", [(1, 1, 1, 1, 0), (5, 4, 13, 3, 1), (40, 30, 300, 16, 2),
-                                                               (1500, 9, 6001, 7, 3), (64, 700, 40000, 64, 4)])
+                                                               (1500, 9, 6001, 7, 3), (64, 700, 40000, 64, 4),
+                                                               (3000, 30, 70001, 3, 5)])
 def test_page_books_against_the_model(lsa, n_rows, max_pages, n_pages, page, seed):
     r = np.random.default_rng(seed)
     pool = Pool(lsa, n_rows, max_pages, n_pages, page)
