@@ -44,39 +44,32 @@ struct QkArgs {
     int32_t lpr;                 // lanes of a row, a power of two
 };
 
-// N consecutive elements to and from fp32.
+// N consecutive elements as they lie in memory, and in fp32.
 template <typename T, int N>
-__device__ __forceinline__ void load_n(const uint8_t *p, float (&x)[N]) {
-    constexpr int kBytes = N * int(sizeof(T));
-    if constexpr (sizeof(T) == 4) {
-        if constexpr (kBytes == 16) {
-            const float4 v = *reinterpret_cast<const float4 *>(p);
-            x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = reinterpret_cast<const float *>(p)[i];
-        }
-    } else {
+struct Raw {
+    static constexpr int kBytes = N * int(sizeof(T)), kWords = (kBytes + 3) / 4;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load(const uint8_t *p) {
         if constexpr (kBytes == 16) {
             const uint4 v = *reinterpret_cast<const uint4 *>(p);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[2 * i] = __uint_as_float(w[i] << 16);
-                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            }
-        } else if constexpr (kBytes >= 4) {
-#pragma unroll
-            for (int i = 0; i < N / 2; ++i) {
-                const uint32_t w = reinterpret_cast<const uint32_t *>(p)[i];
-                x[2 * i] = __uint_as_float(w << 16);
-                x[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
-            }
+            w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+        } else if constexpr (kBytes == 8) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(p);
+            w[0] = v.x; w[1] = v.y;
+        } else if constexpr (kBytes == 4) {
+            w[0] = *reinterpret_cast<const uint32_t *>(p);
         } else {
-            x[0] = bf16_to_f32(*reinterpret_cast<const uint16_t *>(p));
+            w[0] = *reinterpret_cast<const uint16_t *>(p);
         }
     }
-}
+    __device__ __forceinline__ void get(float (&x)[N]) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if constexpr (sizeof(T) == 4) x[i] = __uint_as_float(w[i]);
+            else x[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+        }
+    }
+};
 
 template <typename T, int N>
 __device__ __forceinline__ void store_n(uint8_t *p, const float (&x)[N]) {
@@ -135,11 +128,45 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope(QkArgs a) {
     const int groups = kThreads / a.lpr;              // of this CTA
     const int lane = threadIdx.x & (a.lpr - 1), group = threadIdx.x / a.lpr;
 
+    // an item is a row: token t, row r of its queries, keys, values.  A group's items are `step` apart; the next one's
+    // elements are on their way while one is computed, the first one's while the angles are
+    const int U = a.D / 2 / VP, rest = (a.D - a.rot) / 2;
+    const int items = nt * a.rows, step = groups * gridDim.y, step_t = step / a.rows, step_r = step - step_t * a.rows;
+    int ia[MU], ib[MU];      // element index of a unit's first and second part
+#pragma unroll
+    for (int m = 0; m < MU; ++m) {
+        const int p = (lane + a.lpr * m) * VP;
+        if (a.interleaved) {
+            ia[m] = 2 * p;
+            ib[m] = 2 * p + VP;
+        } else {
+            ia[m] = p < half ? p : a.rot + (p - half);
+            ib[m] = p < half ? p + half : a.rot + rest + (p - half);
+        }
+    }
+    Raw<T, VP> ra[MU], rb[MU];
+    auto fetch = [&](int t, int r) {
+        const int64_t tok = t0 + t;
+        const uint8_t *src = r < a.Hq ? a.q + tok * a.q_stride + int64_t(r) * a.D * E
+                             : r < a.Hq + a.Hkv ? a.k + tok * a.k_stride + int64_t(r - a.Hq) * a.D * E
+                                                : a.v + tok * a.v_stride + int64_t(r - a.Hq - a.Hkv) * a.D * E;
+#pragma unroll
+        for (int m = 0; m < MU; ++m) {
+            if (lane + a.lpr * m < U) {
+                ra[m].load(src + ia[m] * E);
+                rb[m].load(src + ib[m] * E);
+            }
+        }
+    };
+    const int i_first = blockIdx.y * groups + group;
+    int t = i_first / a.rows, r = i_first - t * a.rows;
+
     pdl_launch_dependents();
     pdl_wait();
+    if (i_first < items) fetch(t, r);
     for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-        const int t = i / half, p = i - t * half;
-        const double turns = double(a.pos[t0 + t]) * a.freq[p] * 0.15915494309189533577;   // 1 / (2 pi)
+        const int tt = i / half, p = i - tt * half;
+        const double turns = double(a.pos[t0 + tt]) * a.freq[p] * 0.15915494309189533577;   // 1 / (2 pi)
         float s, c;
         sincospif(float(2.0 * (turns - rint(turns))), &s, &c);
         cs[i] = make_float2(a.mscale * c, a.mscale * a.sign * s);
@@ -164,35 +191,20 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope(QkArgs a) {
     }
     __syncthreads();
 
-    const int U = a.D / 2 / VP, rest = (a.D - a.rot) / 2;
-    const int items = nt * a.rows, step = groups * gridDim.y;
     // every lane of a warp makes the same number of rounds, as the reductions below need all of them
     for (int i0 = blockIdx.y * groups; i0 < items; i0 += step) {
-        const int item = i0 + group;
-        const bool on = item < items;
-        const int t = on ? item / a.rows : 0, r = on ? item - t * a.rows : 0;
+        const bool on = i0 + group < items;
         const int kind = r < a.Hq ? 0 : r < a.Hq + a.Hkv ? 1 : 2;        // query, key, value
         const int h = kind == 0 ? r : kind == 1 ? r - a.Hq : r - a.Hq - a.Hkv;
+        const int tn = on ? t : 0;                                       // (past the last item t has no angles)
         const int64_t tok = t0 + t;
-        const uint8_t *src = kind == 0 ? a.q + tok * a.q_stride : kind == 1 ? a.k + tok * a.k_stride
-                                                                            : a.v + tok * a.v_stride;
-        src += int64_t(h) * a.D * E;
         float xa[MU][VP], xb[MU][VP];
-        int ia[MU], ib[MU];      // element index of a unit's first and second part
         float sum = 0.f;
 #pragma unroll
         for (int m = 0; m < MU; ++m) {
-            const int u = lane + a.lpr * m, p = u * VP;
-            if (a.interleaved) {
-                ia[m] = 2 * p;
-                ib[m] = 2 * p + VP;
-            } else {
-                ia[m] = p < half ? p : a.rot + (p - half);
-                ib[m] = p < half ? p + half : a.rot + rest + (p - half);
-            }
-            if (on && u < U) {
-                load_n<T, VP>(src + ia[m] * E, xa[m]);
-                load_n<T, VP>(src + ib[m] * E, xb[m]);
+            if (on && lane + a.lpr * m < U) {
+                ra[m].get(xa[m]);
+                rb[m].get(xb[m]);
 #pragma unroll
                 for (int e = 0; e < VP; ++e) sum = fmaf(xa[m][e], xa[m][e], fmaf(xb[m][e], xb[m][e], sum));
             } else {
@@ -200,6 +212,13 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope(QkArgs a) {
                 for (int e = 0; e < VP; ++e) xa[m][e] = xb[m][e] = 0.f;
             }
         }
+        t += step_t;
+        r += step_r;
+        if (r >= a.rows) {
+            r -= a.rows;
+            ++t;
+        }
+        if (i0 + step + group < items) fetch(t, r);
         const uint8_t *w = kind == 0 ? a.wq : kind == 1 ? a.wk : nullptr;
         if (a.wq || a.wk)
             for (int x = a.lpr / 2; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
@@ -209,8 +228,11 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope(QkArgs a) {
             for (int m = 0; m < MU; ++m) {
                 if (lane + a.lpr * m < U) {
                     float wa[VP], wb[VP];
-                    load_n<T, VP>(w + ia[m] * E, wa);
-                    load_n<T, VP>(w + ib[m] * E, wb);
+                    Raw<T, VP> x;
+                    x.load(w + ia[m] * E);
+                    x.get(wa);
+                    x.load(w + ib[m] * E);
+                    x.get(wb);
 #pragma unroll
                     for (int e = 0; e < VP; ++e) {
                         xa[m][e] = xa[m][e] * f * wa[e];
@@ -223,7 +245,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope(QkArgs a) {
 #pragma unroll
             for (int m = 0; m < MU; ++m) {
                 const int p = (lane + a.lpr * m) * VP;
-                const float2 *c = cs + t * half + p;
+                const float2 *c = cs + tn * half + p;
                 if (a.interleaved) {
                     float y[2 * VP];
 #pragma unroll
@@ -275,8 +297,8 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope(QkArgs a) {
                     for (int e = 0; e < VP; ++e) amax = fmaxf(amax, fmaxf(fabsf(xa[m][e]), fabsf(xb[m][e])));
                 for (int x = a.lpr / 2; x > 0; x >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, x));
             }
-            if (on && kind != 0 && dst[2 * t] >= 0) {
-                uint8_t *row = (kind == 1 ? a.cache.k : a.cache.v) + dst[2 * t] + h * a.cache.head_stride;
+            if (on && kind != 0 && dst[2 * tn] >= 0) {
+                uint8_t *row = (kind == 1 ? a.cache.k : a.cache.v) + dst[2 * tn] + h * a.cache.head_stride;
                 if (a.append == 1) {
 #pragma unroll
                     for (int m = 0; m < MU; ++m) {
@@ -296,7 +318,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope(QkArgs a) {
                         }
                     }
                     if (lane == 0)
-                        (kind == 1 ? a.cache.ks : a.cache.vs)[dst[2 * t + 1] * a.cache.Hkv + h] = scale;
+                        (kind == 1 ? a.cache.ks : a.cache.vs)[dst[2 * tn + 1] * a.cache.Hkv + h] = scale;
                 }
             }
         }
