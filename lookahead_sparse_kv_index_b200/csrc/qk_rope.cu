@@ -4,12 +4,16 @@
 // written to q_out / k_out and, with the values, to the slots of a paged cache.
 //
 // One pass: a row is read once and written once, so the call is bound by HBM for many tokens and by its latency for
-// few.  A group of LPR lanes owns a row; a lane owns units of VP pairs, i.e. VP elements of the row's first half and
-// the VP that pair with them (or 2 VP neighbours where pairs are interleaved), so rotating needs no exchange between
-// lanes and both accesses are as wide as the sizes allow (16 bytes at VP = 8 bf16 or 4 fp32).  The angles are shared by
-// a token's heads: each CTA first computes the cos and sin of its tokens' pairs into shared memory.  The angle is
-// reduced to a fraction of a turn in fp64 (pos * freq reaches millions of radians, where fp32 keeps no fraction), and
-// only the fraction goes to the fp32 sincospi.
+// few.  A warp does the rows of one token (or a part of them, where tokens are few), LPR lanes a row.  A lane owns units
+// of VP pairs of the row, i.e. VP elements of the rotated part's first half and the VP that pair with them (or 2 VP
+// neighbours where pairs are interleaved), so rotating needs no exchange between lanes and both accesses are as wide as
+// the sizes allow (16 bytes at VP = 8 bf16 or 4 fp32).  As a lane's pairs are the same in every row, the products of its
+// weights with cos and sin stay in registers while the token's heads pass, and a rotation is four products a pair:
+//     a' = f (x_a (m w_a cos) - x_b (m w_b sin)),  b' = f (x_a (m w_a sin) + x_b (m w_b cos)),  f = 1 / sqrt(mean + eps).
+// The warp computes the token's angles once, reduced to a fraction of a turn in fp64 (pos * freq reaches millions of
+// radians, where fp32 keeps no fraction); only the fraction goes to the fp32 sincospi.  (Before that a CTA held the angles
+// of four tokens in shared memory and each row read them and its weights again: 380 instructions for four rows of 128,
+// and 99 us for 16384 tokens of 48 heads, bound by instruction issue.)
 #include <math.h>
 
 #include "paged.cuh"
@@ -25,6 +29,7 @@ struct QkArgs {
     const uint8_t *q, *k, *v;
     uint8_t *q_out, *k_out;
     int64_t q_stride, q_out_stride, k_stride, k_out_stride, v_stride;   // bytes between tokens
+    int32_t row_bytes;           // of a head of q, k, v
     int64_t T;
     int32_t Hq, Hkv, D, rot, interleaved;
     float sign, mscale, eps;
@@ -39,9 +44,9 @@ struct QkArgs {
     int32_t n_rows;
     int64_t reach;
     int32_t *err;
-    int32_t tt;                  // tokens of a CTA
-    int32_t rows;                // rows of a token: Hq + Hkv (+ Hkv)
     int32_t lpr;                 // lanes of a row, a power of two
+    int32_t nq, nk, nv;          // rounds of a token's queries, keys, values: 32 / lpr rows each
+    int32_t parts;               // warps of a token
 };
 
 // N consecutive elements as they lie in memory, and in fp32.
@@ -116,93 +121,98 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&x)[N], floa
     }
 }
 
-// T: element type of q, k, v; VP: pairs of a unit; MU: units of a lane (VP * MU = 8: D <= 512 on 32 lanes).
-template <typename T, int VP>
+// T: element type of q, k, v; VP: pairs of a unit; MU: units of a lane (VP * MU = 8: D <= 512 on 32 lanes); LPR: lanes of
+// a row (0: a.lpr).
+template <typename T, int VP, int LPR>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope(QkArgs a) {
     constexpr int MU = 8 / VP;
     constexpr int E = int(sizeof(T));
-    extern __shared__ float2 cs[];                    // [tt][rot / 2]
-    int64_t *dst = reinterpret_cast<int64_t *>(cs + a.tt * (a.rot / 2));   // [tt][2]: byte offset, flat slot
-    const int64_t t0 = int64_t(blockIdx.x) * a.tt;
-    const int nt = int(a.T - t0 < a.tt ? a.T - t0 : a.tt), half = a.rot / 2;
-    const int groups = kThreads / a.lpr;              // of this CTA
-    const int lane = threadIdx.x & (a.lpr - 1), group = threadIdx.x / a.lpr;
+    extern __shared__ float2 angles[];                // [warps][rot / 2]
+    const int lpr = LPR ? LPR : a.lpr, half = a.rot / 2, U = a.D / 2 / VP, rest = (a.D - a.rot) / 2;
+    const int wl = threadIdx.x & 31, lane = wl & (lpr - 1), group = wl / lpr, groups = 32 / lpr;
+    const int64_t item = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    const int64_t tok = item / a.parts;
+    const int part = int(item - tok * a.parts), rounds = a.nq + a.nk + a.nv;
+    const int begin = part * rounds / a.parts, end = (part + 1) * rounds / a.parts;
 
-    // an item is a row: token t, row r of its queries, keys, values.  A group's items are `step` apart; the next one's
-    // elements are on their way while one is computed, the first one's while the angles are
-    const int U = a.D / 2 / VP, rest = (a.D - a.rot) / 2;
-    const int items = nt * a.rows, step = groups * gridDim.y, step_t = step / a.rows, step_r = step - step_t * a.rows;
-    int ia[MU], ib[MU];      // element index of a unit's first and second part
+    int ia[MU], ib[MU];      // byte offset of a unit's first and second part
+    bool mine[MU], turns[MU];
 #pragma unroll
     for (int m = 0; m < MU; ++m) {
-        const int p = (lane + a.lpr * m) * VP;
+        const int u = lane + lpr * m, p = u * VP;
+        mine[m] = u < U;
+        turns[m] = p < half;
         if (a.interleaved) {
-            ia[m] = 2 * p;
-            ib[m] = 2 * p + VP;
+            ia[m] = 2 * p * E;
+            ib[m] = (2 * p + VP) * E;
         } else {
-            ia[m] = p < half ? p : a.rot + (p - half);
-            ib[m] = p < half ? p + half : a.rot + rest + (p - half);
+            ia[m] = (p < half ? p : a.rot + (p - half)) * E;
+            ib[m] = (p < half ? p + half : a.rot + rest + (p - half)) * E;
         }
     }
-    Raw<T, VP> ra[MU], rb[MU];
-    auto fetch = [&](int t, int r) {
-        const int64_t tok = t0 + t;
-        const uint8_t *src = r < a.Hq ? a.q + tok * a.q_stride + int64_t(r) * a.D * E
-                             : r < a.Hq + a.Hkv ? a.k + tok * a.k_stride + int64_t(r - a.Hq) * a.D * E
-                                                : a.v + tok * a.v_stride + int64_t(r - a.Hq - a.Hkv) * a.D * E;
-#pragma unroll
-        for (int m = 0; m < MU; ++m) {
-            if (lane + a.lpr * m < U) {
-                ra[m].load(src + ia[m] * E);
-                rb[m].load(src + ib[m] * E);
-            }
-        }
-    };
-    const int i_first = blockIdx.y * groups + group;
-    int t = i_first / a.rows, r = i_first - t * a.rows;
+    // round rd is rows (rd - start of its kind) * groups + group of the token's queries, keys or values
+    auto kind_of = [&](int rd) { return rd < a.nq ? 0 : rd < a.nq + a.nk ? 1 : 2; };
+    auto head_of = [&](int rd) { return (rd - (rd < a.nq ? 0 : rd < a.nq + a.nk ? a.nq : a.nq + a.nk)) * groups + group; };
 
     pdl_launch_dependents();
     pdl_wait();
-    if (i_first < items) fetch(t, r);
-    for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-        const int tt = i / half, p = i - tt * half;
-        const double turns = double(a.pos[t0 + tt]) * a.freq[p] * 0.15915494309189533577;   // 1 / (2 pi)
-        float s, c;
-        sincospif(float(2.0 * (turns - rint(turns))), &s, &c);
-        cs[i] = make_float2(a.mscale * c, a.mscale * a.sign * s);
-    }
-    if (a.append && threadIdx.x < nt) {
-        const int64_t t = t0 + threadIdx.x;
-        const int64_t row = a.seq ? a.seq[t] : t, at = a.at[t];
-        int64_t off = -1, slot = 0;
+    if (tok >= a.T) return;
+    Raw<T, VP> ra[MU], rb[MU];      // the next round's elements, on their way while one round is computed
+    auto fetch = [&](int rd) {
+        const int kind = kind_of(rd), h = head_of(rd);
+        const uint8_t *src = kind == 0 ? a.q + tok * a.q_stride : kind == 1 ? a.k + tok * a.k_stride
+                                                                            : a.v + tok * a.v_stride;
+        if (h < (kind == 0 ? a.Hq : a.Hkv)) {
+            src += int64_t(h) * a.row_bytes;
+#pragma unroll
+            for (int m = 0; m < MU; ++m) {
+                if (mine[m]) {
+                    ra[m].load(src + ia[m]);
+                    rb[m].load(src + ib[m]);
+                }
+            }
+        }
+    };
+    if (begin < end) fetch(begin);
+
+    // where the token goes in the cache (every lane finds it)
+    int64_t off = -1, slot = 0;
+    if (a.append && end > a.nq) {
+        const int64_t row = a.seq ? a.seq[tok] : tok, at = a.at[tok];
         if (row >= 0 && at >= 0) {
             int64_t page = -1;
-            if (row < a.n_rows && at < a.reach) page = a.table[row * a.table_stride + at / a.cache.page_size];
+            const int s = row < a.n_rows && at < a.reach ? int(uint32_t(at) % uint32_t(a.cache.page_size)) : 0;
+            if (row < a.n_rows && at < a.reach) page = a.table[row * a.table_stride + uint32_t(at) / uint32_t(a.cache.page_size)];
             if (page >= 0 && page < a.cache.n_pages) {
-                const int s = int(at % a.cache.page_size);
                 off = page * a.cache.page_stride + s * a.cache.slot_stride;
                 slot = page * a.cache.page_size + s;
-            } else {
+            } else if (wl == 0) {
                 raise_err(a.err, LSA_ERR_INVALID);
             }
         }
-        dst[2 * threadIdx.x] = off;
-        dst[2 * threadIdx.x + 1] = slot;
     }
-    __syncthreads();
+    float2 *cs = angles + (threadIdx.x >> 5) * half;
+    if (begin < a.nq + a.nk) {
+        for (int i = wl; i < half; i += 32) {
+            const double turn = double(a.pos[tok]) * a.freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
+            float s, c;
+            sincospif(float(2.0 * (turn - rint(turn))), &s, &c);
+            cs[i] = make_float2(a.mscale * c, a.mscale * a.sign * s);
+        }
+        __syncwarp();
+    }
 
-    // every lane of a warp makes the same number of rounds, as the reductions below need all of them
-    for (int i0 = blockIdx.y * groups; i0 < items; i0 += step) {
-        const bool on = i0 + group < items;
-        const int kind = r < a.Hq ? 0 : r < a.Hq + a.Hkv ? 1 : 2;        // query, key, value
-        const int h = kind == 0 ? r : kind == 1 ? r - a.Hq : r - a.Hq - a.Hkv;
-        const int tn = on ? t : 0;                                       // (past the last item t has no angles)
-        const int64_t tok = t0 + t;
+    float ac[MU][VP], as[MU][VP], bc[MU][VP], bs[MU][VP];   // weights times cos and sin, of a unit's two parts
+    int weights_of = -1;
+    for (int rd = begin; rd < end; ++rd) {
+        const int kind = kind_of(rd), h = head_of(rd);
+        const bool on = h < (kind == 0 ? a.Hq : a.Hkv);
+        const uint8_t *w = kind == 0 ? a.wq : kind == 1 ? a.wk : nullptr;
         float xa[MU][VP], xb[MU][VP];
         float sum = 0.f;
 #pragma unroll
         for (int m = 0; m < MU; ++m) {
-            if (on && lane + a.lpr * m < U) {
+            if (on && mine[m]) {
                 ra[m].get(xa[m]);
                 rb[m].get(xb[m]);
 #pragma unroll
@@ -212,125 +222,144 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope(QkArgs a) {
                 for (int e = 0; e < VP; ++e) xa[m][e] = xb[m][e] = 0.f;
             }
         }
-        t += step_t;
-        r += step_r;
-        if (r >= a.rows) {
-            r -= a.rows;
-            ++t;
-        }
-        if (i0 + step + group < items) fetch(t, r);
-        const uint8_t *w = kind == 0 ? a.wq : kind == 1 ? a.wk : nullptr;
-        if (a.wq || a.wk)
-            for (int x = a.lpr / 2; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-        if (w) {
-            const float f = 1.f / sqrtf(sum / float(a.D) + a.eps);
+        if (rd + 1 < end) fetch(rd + 1);
+        if (kind != 2) {
+            if (kind != weights_of) {
+                weights_of = kind;
 #pragma unroll
-            for (int m = 0; m < MU; ++m) {
-                if (lane + a.lpr * m < U) {
+                for (int m = 0; m < MU; ++m) {
                     float wa[VP], wb[VP];
-                    Raw<T, VP> x;
-                    x.load(w + ia[m] * E);
-                    x.get(wa);
-                    x.load(w + ib[m] * E);
-                    x.get(wb);
+                    if (w && mine[m]) {
+                        Raw<T, VP> x;
+                        x.load(w + ia[m]);
+                        x.get(wa);
+                        x.load(w + ib[m]);
+                        x.get(wb);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < VP; ++e) wa[e] = wb[e] = 1.f;
+                    }
 #pragma unroll
                     for (int e = 0; e < VP; ++e) {
-                        xa[m][e] = xa[m][e] * f * wa[e];
-                        xb[m][e] = xb[m][e] * f * wb[e];
+                        const int p = (lane + lpr * m) * VP + e;
+                        // element pairs (a, b) of interleaved units are neighbours, in both parts of the unit
+                        const float2 c = turns[m] ? cs[p] : make_float2(1.f, 0.f);
+                        const float u = a.interleaved ? (e < VP / 2 || VP == 1 ? wa[2 * e % VP] : wb[2 * e % VP]) : wa[e];
+                        const float v = a.interleaved ? (VP == 1 ? wb[0] : e < VP / 2 ? wa[(2 * e + 1) % VP] : wb[(2 * e + 1) % VP])
+                                                      : wb[e];
+                        ac[m][e] = u * c.x;
+                        as[m][e] = u * c.y;
+                        bc[m][e] = v * c.x;
+                        bs[m][e] = v * c.y;
                     }
                 }
             }
-        }
-        if (kind != 2 && half) {
+            float f = 1.f;
+            if (w) {
+#pragma unroll
+                for (int x = 16; x > 0; x >>= 1)
+                    if (x < lpr) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                f = rsqrtf(sum / float(a.D) + a.eps);
+            }
 #pragma unroll
             for (int m = 0; m < MU; ++m) {
-                const int p = (lane + a.lpr * m) * VP;
-                const float2 *c = cs + tn * half + p;
-                if (a.interleaved) {
-                    float y[2 * VP];
+                float y[2 * VP];
 #pragma unroll
-                    for (int e = 0; e < VP; ++e) {
-                        y[e] = xa[m][e];
-                        y[VP + e] = xb[m][e];
+                for (int e = 0; e < VP; ++e) {
+                    y[e] = xa[m][e];
+                    y[VP + e] = xb[m][e];
+                }
+#pragma unroll
+                for (int e = 0; e < VP; ++e) {
+                    const float x0 = a.interleaved ? y[2 * e] : y[e], x1 = a.interleaved ? y[2 * e + 1] : y[VP + e];
+                    float p = x0 * ac[m][e], q = x1 * bc[m][e];
+                    if (turns[m]) {       // (an element that does not turn never meets its partner)
+                        p = fmaf(-x1, bs[m][e], p);
+                        q = fmaf(x0, as[m][e], q);
                     }
+                    xa[m][e] = p * f;
+                    xb[m][e] = q * f;
+                }
+                if (a.interleaved) {      // back to the order of the row
 #pragma unroll
                     for (int e = 0; e < VP; ++e) {
-                        if (p + e < half) {
-                            const float x0 = y[2 * e], x1 = y[2 * e + 1];
-                            y[2 * e] = x0 * c[e].x - x1 * c[e].y;
-                            y[2 * e + 1] = x0 * c[e].y + x1 * c[e].x;
-                        }
+                        y[2 * e] = xa[m][e];
+                        y[2 * e + 1] = xb[m][e];
                     }
 #pragma unroll
                     for (int e = 0; e < VP; ++e) {
                         xa[m][e] = y[e];
                         xb[m][e] = y[VP + e];
                     }
-                } else if (p < half) {
+                }
+            }
+            uint8_t *out = kind == 0 ? a.q_out + tok * a.q_out_stride : a.k_out ? a.k_out + tok * a.k_out_stride : nullptr;
+            if (on && out) {
+                out += int64_t(h) * a.row_bytes;
 #pragma unroll
-                    for (int e = 0; e < VP; ++e) {
-                        const float x0 = xa[m][e], x1 = xb[m][e];
-                        xa[m][e] = x0 * c[e].x - x1 * c[e].y;
-                        xb[m][e] = x0 * c[e].y + x1 * c[e].x;
+                for (int m = 0; m < MU; ++m) {
+                    if (mine[m]) {
+                        store_n<T, VP>(out + ia[m], xa[m]);
+                        store_n<T, VP>(out + ib[m], xb[m]);
                     }
                 }
             }
         }
-        uint8_t *out = kind == 0 ? a.q_out + tok * a.q_out_stride
-                                 : kind == 1 && a.k_out ? a.k_out + tok * a.k_out_stride : nullptr;
-        if (on && out) {
-            out += int64_t(h) * a.D * E;
+        if (kind != 0 && off >= 0) {
+            uint8_t *row = (kind == 1 ? a.cache.k : a.cache.v) + off + h * a.cache.head_stride;
+            if (a.append == 1) {
+                if (on) {
 #pragma unroll
-            for (int m = 0; m < MU; ++m) {
-                if (lane + a.lpr * m < U) {
-                    store_n<T, VP>(out + ia[m] * E, xa[m]);
-                    store_n<T, VP>(out + ib[m] * E, xb[m]);
+                    for (int m = 0; m < MU; ++m) {
+                        if (mine[m]) {
+                            store_n<T, VP>(row + ia[m], xa[m]);
+                            store_n<T, VP>(row + ib[m], xb[m]);
+                        }
+                    }
                 }
-            }
-        }
-        if (a.append) {
-            float amax = 0.f;
-            if (a.append == 2) {
+            } else {
+                float amax = 0.f;
 #pragma unroll
                 for (int m = 0; m < MU; ++m)
 #pragma unroll
                     for (int e = 0; e < VP; ++e) amax = fmaxf(amax, fmaxf(fabsf(xa[m][e]), fabsf(xb[m][e])));
-                for (int x = a.lpr / 2; x > 0; x >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, x));
-            }
-            if (on && kind != 0 && dst[2 * tn] >= 0) {
-                uint8_t *row = (kind == 1 ? a.cache.k : a.cache.v) + dst[2 * tn] + h * a.cache.head_stride;
-                if (a.append == 1) {
+#pragma unroll
+                for (int x = 16; x > 0; x >>= 1)
+                    if (x < lpr) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, x));
+                // (a row of tiny values keeps a normal scale, so that 0 / scale is 0)
+                const float scale = amax > 0.f ? fmaxf(amax / 448.f, 1.17549435e-38f) : 1.f;
+                if (on) {
 #pragma unroll
                     for (int m = 0; m < MU; ++m) {
-                        if (lane + a.lpr * m < U) {
-                            store_n<T, VP>(row + ia[m] * E, xa[m]);
-                            store_n<T, VP>(row + ib[m] * E, xb[m]);
+                        if (mine[m]) {
+                            store_e4m3<VP>(row + ia[m] / E, xa[m], scale);
+                            store_e4m3<VP>(row + ib[m] / E, xb[m], scale);
                         }
                     }
-                } else {
-                    // (a row of tiny values keeps a normal scale, so that 0 / scale is 0)
-                    const float scale = amax > 0.f ? fmaxf(amax / 448.f, 1.17549435e-38f) : 1.f;
-#pragma unroll
-                    for (int m = 0; m < MU; ++m) {
-                        if (lane + a.lpr * m < U) {
-                            store_e4m3<VP>(row + ia[m], xa[m], scale);
-                            store_e4m3<VP>(row + ib[m], xb[m], scale);
-                        }
-                    }
-                    if (lane == 0)
-                        (kind == 1 ? a.cache.ks : a.cache.vs)[dst[2 * tn + 1] * a.cache.Hkv + h] = scale;
+                    if (lane == 0) (kind == 1 ? a.cache.ks : a.cache.vs)[slot * a.cache.Hkv + h] = scale;
                 }
             }
         }
     }
 }
 
-template <typename T, int VP>
-lsa_status launch_vp(const QkArgs &a, dim3 grid, size_t smem, cudaStream_t st) {
-    LSA_CUDA(ensure_smem(qk_norm_rope<T, VP>, smem));
-    LSA_CUDA(launch_pdl(qk_norm_rope<T, VP>, grid, dim3(kThreads), smem, st, a));
+template <typename T, int VP, int LPR>
+lsa_status launch_as(const QkArgs &a, unsigned grid, size_t smem, cudaStream_t st) {
+    LSA_CUDA(ensure_smem(qk_norm_rope<T, VP, LPR>, smem));
+    LSA_CUDA(launch_pdl(qk_norm_rope<T, VP, LPR>, dim3(grid), dim3(kThreads), smem, st, a));
     LSA_LAUNCHED("qk_norm_rope");
     return LSA_OK;
+}
+// The usual head dims have the lanes of a row at compile time (64, 128 and 256 elements at the widest unit).
+template <typename T, int VP>
+lsa_status launch_vp(const QkArgs &a, unsigned grid, size_t smem, cudaStream_t st) {
+    if constexpr (VP * sizeof(T) == 16) {
+        constexpr int kRow = 128 / 2 / VP;
+        if (a.lpr == kRow / 2) return launch_as<T, VP, kRow / 2>(a, grid, smem, st);
+        if (a.lpr == kRow) return launch_as<T, VP, kRow>(a, grid, smem, st);
+        if (a.lpr == 2 * kRow) return launch_as<T, VP, 2 * kRow>(a, grid, smem, st);
+    }
+    return launch_as<T, VP, 0>(a, grid, smem, st);
 }
 
 }  // namespace
@@ -432,23 +461,25 @@ extern "C" lsa_status lsa_qk_norm_rope(const void *q, int64_t q_stride, void *q_
     a.table_stride = table_stride;
     a.n_rows = n_rows;
     a.err = err;
-    a.rows = Hq + a.Hkv + (v ? Hkv : 0);
-    // the widest unit that the sizes allow
+    a.row_bytes = int32_t(D * e);
+    // the widest unit that the sizes allow, of pairs that all turn or all stay
     int vp = dtype == LSA_BF16 ? 8 : 4;
-    auto fits = [&](int n) { return a.interleaved ? D / 2 % n == 0 : rot / 2 % n == 0 && (D - rot) / 2 % n == 0; };
+    auto fits = [&](int n) { return rot / 2 % n == 0 && (D - rot) / 2 % n == 0; };
     while (!fits(vp)) vp /= 2;
     a.lpr = 1;
     while (a.lpr < 32 && a.lpr * vp < D / 2) a.lpr *= 2;
-    const int groups = kThreads / a.lpr;
-    // tokens of a CTA: enough CTAs to fill the device, else one token, and then its rows over several
-    const int64_t per = (int64_t(a.rows) + groups - 1) / groups;
-    a.tt = 1;
-    while (a.tt < 4 && T / (2 * a.tt) >= int64_t(sm_count()) * 8) a.tt *= 2;
-    int gy = 1;
-    if (a.tt == 1)
-        while (gy < per && T * gy < int64_t(sm_count()) * 4) ++gy;
-    const dim3 grid(unsigned((T + a.tt - 1) / a.tt), gy);
-    const size_t smem = size_t(a.tt) * (rot / 2) * 8 + size_t(a.tt) * 16;
+    const int groups = 32 / a.lpr;
+    a.nq = (Hq + groups - 1) / groups;
+    a.nk = (a.Hkv + groups - 1) / groups;
+    a.nv = v ? a.nk : 0;
+    // a warp a token, or several until the device has warps enough (16 an SM)
+    const int rounds = a.nq + a.nk + a.nv;
+    const int64_t want = int64_t(sm_count()) * 16 / T;
+    a.parts = int32_t(want < 1 ? 1 : want < rounds ? want : rounds);
+    const int64_t items = T * a.parts;
+    constexpr int kWarps = kThreads / 32;
+    const unsigned grid = unsigned((items + kWarps - 1) / kWarps);
+    const size_t smem = size_t(kWarps) * (rot / 2) * 8;
     cudaStream_t st = as_stream(stream);
     if (dtype == LSA_BF16) {
         switch (vp) {
