@@ -8,7 +8,8 @@
 // of VP pairs of the row, i.e. VP elements of the rotated part's first half and the VP that pair with them (or 2 VP
 // neighbours where pairs are interleaved), so rotating needs no exchange between lanes and both accesses are as wide as
 // the sizes allow (16 bytes at VP = 8 bf16 or 4 fp32).  As a lane's pairs are the same in every row, the products of its
-// weights with cos and sin stay in registers while the token's heads pass, and a rotation is four products a pair:
+// weights with cos and sin stay in registers while the token's heads pass (its rows come through a ring of cp.async copies
+// in shared memory, which each lane reads back itself), and a rotation is four products a pair:
 //     a' = f (x_a (m w_a cos) - x_b (m w_b sin)),  b' = f (x_a (m w_a sin) + x_b (m w_b cos)),  f = 1 / sqrt(mean + eps).
 // The warp computes the token's angles once, reduced to a fraction of a turn in fp64 (pos * freq reaches millions of
 // radians, where fp32 keeps no fraction); only the fraction goes to the fp32 sincospi.  (Before that a CTA held the angles
@@ -23,7 +24,8 @@ namespace {
 
 using paged::CacheView;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
+constexpr int kAhead = 4;            // rounds of a warp in its ring: three on their way while one is computed
 
 struct QkArgs {
     const uint8_t *q, *k, *v;
@@ -32,7 +34,7 @@ struct QkArgs {
     int32_t row_bytes;           // of a head of q, k, v
     int64_t T;
     int32_t Hq, Hkv, D, rot, interleaved;
-    float sign, mscale, eps;
+    float sign, mscale, eps, inv_d;
     const uint8_t *wq, *wk;
     const int32_t *pos;
     const double *freq;
@@ -66,6 +68,14 @@ struct Raw {
         } else {
             w[0] = *reinterpret_cast<const uint16_t *>(p);
         }
+    }
+    // Global to shared memory, asynchronously where the size allows it.
+    static __device__ __forceinline__ void copy(uint8_t *to, const uint8_t *from) {
+        const uint32_t at = uint32_t(__cvta_generic_to_shared(to));
+        if constexpr (kBytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+        else if constexpr (kBytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at), "l"(from) : "memory");
+        else if constexpr (kBytes == 4) asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at), "l"(from) : "memory");
+        else *reinterpret_cast<uint16_t *>(to) = *reinterpret_cast<const uint16_t *>(from);
     }
     __device__ __forceinline__ void get(float (&x)[N]) const {
 #pragma unroll
@@ -121,19 +131,19 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&x)[N], floa
     }
 }
 
-// T: element type of q, k, v; VP: pairs of a unit; MU: units of a lane (VP * MU = 8: D <= 512 on 32 lanes); LPR: lanes of
-// a row (0: a.lpr).
-template <typename T, int VP, int LPR>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope(QkArgs a) {
-    constexpr int MU = 8 / VP;
+// T: element type of q, k, v; VP: pairs of a unit; MU: units of a lane; LPR: lanes of a row (0: a.lpr); IL: interleaved
+// pairs.
+template <typename T, int VP, int MU, int LPR, bool IL>
+__global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(QkArgs a) {
     constexpr int E = int(sizeof(T));
-    extern __shared__ float2 angles[];                // [warps][rot / 2]
+    constexpr int kPart = VP * E, kSlot = 32 * 2 * MU * kPart;
+    extern __shared__ __align__(16) uint8_t smem[];   // [warps] rings of kAhead rounds, then the angles [warps][rot / 2]
     const int lpr = LPR ? LPR : a.lpr, half = a.rot / 2, U = a.D / 2 / VP, rest = (a.D - a.rot) / 2;
     const int wl = threadIdx.x & 31, lane = wl & (lpr - 1), group = wl / lpr, groups = 32 / lpr;
-    const int64_t item = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-    const int64_t tok = item / a.parts;
-    const int part = int(item - tok * a.parts), rounds = a.nq + a.nk + a.nv;
-    const int begin = part * rounds / a.parts, end = (part + 1) * rounds / a.parts;
+    const uint32_t item = blockIdx.x * kWarps + (threadIdx.x >> 5), token = item / uint32_t(a.parts);
+    const int64_t tok = token;
+    const int part = int(item - token * a.parts), rounds = a.nq + a.nk + a.nv;
+    const int begin = a.parts == 1 ? 0 : part * rounds / a.parts, end = a.parts == 1 ? rounds : (part + 1) * rounds / a.parts;
 
     int ia[MU], ib[MU];      // byte offset of a unit's first and second part
     bool mine[MU], turns[MU];
@@ -142,7 +152,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope(QkArgs a) {
         const int u = lane + lpr * m, p = u * VP;
         mine[m] = u < U;
         turns[m] = p < half;
-        if (a.interleaved) {
+        if (IL) {
             ia[m] = 2 * p * E;
             ib[m] = (2 * p + VP) * E;
         } else {
@@ -150,30 +160,58 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope(QkArgs a) {
             ib[m] = (p < half ? p + half : a.rot + rest + (p - half)) * E;
         }
     }
-    // round rd is rows (rd - start of its kind) * groups + group of the token's queries, keys or values
-    auto kind_of = [&](int rd) { return rd < a.nq ? 0 : rd < a.nq + a.nk ? 1 : 2; };
-    auto head_of = [&](int rd) { return (rd - (rd < a.nq ? 0 : rd < a.nq + a.nk ? a.nq : a.nq + a.nk)) * groups + group; };
-
     pdl_launch_dependents();
     pdl_wait();
     if (tok >= a.T) return;
-    Raw<T, VP> ra[MU], rb[MU];      // the next round's elements, on their way while one round is computed
-    auto fetch = [&](int rd) {
-        const int kind = kind_of(rd), h = head_of(rd);
-        const uint8_t *src = kind == 0 ? a.q + tok * a.q_stride : kind == 1 ? a.k + tok * a.k_stride
-                                                                            : a.v + tok * a.v_stride;
-        if (h < (kind == 0 ? a.Hq : a.Hkv)) {
-            src += int64_t(h) * a.row_bytes;
+    // the token's rounds are its queries' (kind 0), keys' and values', `groups` rows each; the next rounds' elements are on
+    // their way while one is computed (a lane without a unit keeps zeros in the ring, a row that is not there what was there
+    // before, and neither is stored)
+    uint8_t *ring = smem + (threadIdx.x >> 5) * (kAhead * kSlot) + wl * kPart;
 #pragma unroll
-            for (int m = 0; m < MU; ++m) {
-                if (mine[m]) {
-                    ra[m].load(src + ia[m]);
-                    rb[m].load(src + ib[m]);
+    for (int m = 0; m < MU; ++m) {
+        if (!mine[m]) {
+            for (int s = 0; s < kAhead; ++s)
+                for (int i = 0; i < kPart; i += 2) {
+                    *reinterpret_cast<uint16_t *>(ring + s * kSlot + 2 * m * 32 * kPart + i) = 0;
+                    *reinterpret_cast<uint16_t *>(ring + s * kSlot + (2 * m + 1) * 32 * kPart + i) = 0;
+                }
+        }
+    }
+    auto source = [&](int kind, int h) {
+        return (kind == 0 ? a.q + tok * a.q_stride : kind == 1 ? a.k + tok * a.k_stride : a.v + tok * a.v_stride) +
+               int64_t(h) * a.row_bytes;
+    };
+    const int step = groups * a.row_bytes;
+    int rd = begin, kind = begin < a.nq ? 0 : begin < a.nq + a.nk ? 1 : 2;
+    int first = kind == 0 ? 0 : kind == 1 ? a.nq : a.nq + a.nk;            // the kind's first round
+    int h = (rd - first) * groups + group, heads = kind == 0 ? a.Hq : a.Hkv;
+    // the fetching side's place
+    int f_rd = begin, f_kind = kind, f_h = h, f_last = first + (kind == 0 ? a.nq : kind == 1 ? a.nk : a.nv);
+    const uint8_t *src = source(kind, h);
+    auto fetch = [&](int slot) {
+        if (f_rd < end) {
+            if (f_h < (f_kind == 0 ? a.Hq : a.Hkv)) {
+#pragma unroll
+                for (int m = 0; m < MU; ++m) {
+                    if (mine[m]) {
+                        Raw<T, VP>::copy(ring + slot * kSlot + 2 * m * 32 * kPart, src + ia[m]);
+                        Raw<T, VP>::copy(ring + slot * kSlot + (2 * m + 1) * 32 * kPart, src + ib[m]);
+                    }
                 }
             }
+            f_h += groups;
+            src += step;
+            if (++f_rd == f_last) {
+                ++f_kind;
+                f_h = group;
+                f_last += f_kind == 1 ? a.nk : a.nv;
+                if (f_rd < end) src = source(f_kind, group);
+            }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    if (begin < end) fetch(begin);
+    for (int s = 0; s < kAhead - 1; ++s) fetch(s);
+    int now = 0;
 
     // where the token goes in the cache (every lane finds it)
     int64_t off = -1, slot = 0;
@@ -191,7 +229,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope(QkArgs a) {
             }
         }
     }
-    float2 *cs = angles + (threadIdx.x >> 5) * half;
+    float2 *cs = reinterpret_cast<float2 *>(smem + kWarps * kAhead * kSlot) + (threadIdx.x >> 5) * half;
     if (begin < a.nq + a.nk) {
         for (int i = wl; i < half; i += 32) {
             const double turn = double(a.pos[tok]) * a.freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
@@ -203,163 +241,177 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope(QkArgs a) {
     }
 
     float ac[MU][VP], as[MU][VP], bc[MU][VP], bs[MU][VP];   // weights times cos and sin, of a unit's two parts
-    int weights_of = -1;
-    for (int rd = begin; rd < end; ++rd) {
-        const int kind = kind_of(rd), h = head_of(rd);
-        const bool on = h < (kind == 0 ? a.Hq : a.Hkv);
+    while (rd < end) {
+        const int last = min(end, first + (kind == 0 ? a.nq : kind == 1 ? a.nk : a.nv));
         const uint8_t *w = kind == 0 ? a.wq : kind == 1 ? a.wk : nullptr;
-        float xa[MU][VP], xb[MU][VP];
-        float sum = 0.f;
-#pragma unroll
-        for (int m = 0; m < MU; ++m) {
-            if (on && mine[m]) {
-                ra[m].get(xa[m]);
-                rb[m].get(xb[m]);
-#pragma unroll
-                for (int e = 0; e < VP; ++e) sum = fmaf(xa[m][e], xa[m][e], fmaf(xb[m][e], xb[m][e], sum));
-            } else {
-#pragma unroll
-                for (int e = 0; e < VP; ++e) xa[m][e] = xb[m][e] = 0.f;
-            }
-        }
-        if (rd + 1 < end) fetch(rd + 1);
+        uint8_t *out = kind == 0 ? a.q_out + tok * a.q_out_stride
+                                 : kind == 1 && a.k_out ? a.k_out + tok * a.k_out_stride : nullptr;
+        if (out) out += int64_t(h) * a.row_bytes;
+        uint8_t *cache = kind != 0 && off >= 0 ? (kind == 1 ? a.cache.k : a.cache.v) + off + h * a.cache.head_stride : nullptr;
         if (kind != 2) {
-            if (kind != weights_of) {
-                weights_of = kind;
-#pragma unroll
-                for (int m = 0; m < MU; ++m) {
-                    float wa[VP], wb[VP];
-                    if (w && mine[m]) {
-                        Raw<T, VP> x;
-                        x.load(w + ia[m]);
-                        x.get(wa);
-                        x.load(w + ib[m]);
-                        x.get(wb);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < VP; ++e) wa[e] = wb[e] = 1.f;
-                    }
-#pragma unroll
-                    for (int e = 0; e < VP; ++e) {
-                        const int p = (lane + lpr * m) * VP + e;
-                        // element pairs (a, b) of interleaved units are neighbours, in both parts of the unit
-                        const float2 c = turns[m] ? cs[p] : make_float2(1.f, 0.f);
-                        const float u = a.interleaved ? (e < VP / 2 || VP == 1 ? wa[2 * e % VP] : wb[2 * e % VP]) : wa[e];
-                        const float v = a.interleaved ? (VP == 1 ? wb[0] : e < VP / 2 ? wa[(2 * e + 1) % VP] : wb[(2 * e + 1) % VP])
-                                                      : wb[e];
-                        ac[m][e] = u * c.x;
-                        as[m][e] = u * c.y;
-                        bc[m][e] = v * c.x;
-                        bs[m][e] = v * c.y;
-                    }
-                }
-            }
-            float f = 1.f;
-            if (w) {
-#pragma unroll
-                for (int x = 16; x > 0; x >>= 1)
-                    if (x < lpr) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-                f = rsqrtf(sum / float(a.D) + a.eps);
-            }
 #pragma unroll
             for (int m = 0; m < MU; ++m) {
-                float y[2 * VP];
+                float wt[2 * VP];        // of the unit's elements, in the order of the row where pairs are neighbours
+                if (w && mine[m]) {
+                    float y[VP];
+                    Raw<T, VP> x;
+                    x.load(w + ia[m]);
+                    x.get(y);
 #pragma unroll
-                for (int e = 0; e < VP; ++e) {
-                    y[e] = xa[m][e];
-                    y[VP + e] = xb[m][e];
+                    for (int e = 0; e < VP; ++e) wt[e] = y[e];
+                    x.load(w + ib[m]);
+                    x.get(y);
+#pragma unroll
+                    for (int e = 0; e < VP; ++e) wt[VP + e] = y[e];
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 2 * VP; ++e) wt[e] = 1.f;
                 }
 #pragma unroll
                 for (int e = 0; e < VP; ++e) {
-                    const float x0 = a.interleaved ? y[2 * e] : y[e], x1 = a.interleaved ? y[2 * e + 1] : y[VP + e];
-                    float p = x0 * ac[m][e], q = x1 * bc[m][e];
-                    if (turns[m]) {       // (an element that does not turn never meets its partner)
-                        p = fmaf(-x1, bs[m][e], p);
-                        q = fmaf(x0, as[m][e], q);
-                    }
-                    xa[m][e] = p * f;
-                    xb[m][e] = q * f;
-                }
-                if (a.interleaved) {      // back to the order of the row
-#pragma unroll
-                    for (int e = 0; e < VP; ++e) {
-                        y[2 * e] = xa[m][e];
-                        y[2 * e + 1] = xb[m][e];
-                    }
-#pragma unroll
-                    for (int e = 0; e < VP; ++e) {
-                        xa[m][e] = y[e];
-                        xb[m][e] = y[VP + e];
-                    }
-                }
-            }
-            uint8_t *out = kind == 0 ? a.q_out + tok * a.q_out_stride : a.k_out ? a.k_out + tok * a.k_out_stride : nullptr;
-            if (on && out) {
-                out += int64_t(h) * a.row_bytes;
-#pragma unroll
-                for (int m = 0; m < MU; ++m) {
-                    if (mine[m]) {
-                        store_n<T, VP>(out + ia[m], xa[m]);
-                        store_n<T, VP>(out + ib[m], xb[m]);
-                    }
+                    const float2 c = turns[m] ? cs[(lane + lpr * m) * VP + e] : make_float2(1.f, 0.f);
+                    const float u = IL ? wt[2 * e] : wt[e], v = IL ? wt[2 * e + 1] : wt[VP + e];
+                    ac[m][e] = u * c.x;
+                    as[m][e] = u * c.y;
+                    bc[m][e] = v * c.x;
+                    bs[m][e] = v * c.y;
                 }
             }
         }
-        if (kind != 0 && off >= 0) {
-            uint8_t *row = (kind == 1 ? a.cache.k : a.cache.v) + off + h * a.cache.head_stride;
-            if (a.append == 1) {
-                if (on) {
+#pragma unroll 1
+        for (; rd < last; ++rd, h += groups) {
+            const bool on = h < heads;
+            float x[MU][2 * VP];         // the unit's first part, then its second
+            float sum = 0.f;
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 2) : "memory");
+            const uint8_t *at = ring + now * kSlot;
 #pragma unroll
-                    for (int m = 0; m < MU; ++m) {
-                        if (mine[m]) {
-                            store_n<T, VP>(row + ia[m], xa[m]);
-                            store_n<T, VP>(row + ib[m], xb[m]);
-                        }
-                    }
-                }
-            } else {
-                float amax = 0.f;
+            for (int m = 0; m < MU; ++m) {
+                float y[VP];
+                Raw<T, VP> r;
+                r.load(at + 2 * m * 32 * kPart);
+                r.get(y);
+#pragma unroll
+                for (int e = 0; e < VP; ++e) x[m][e] = y[e];
+                r.load(at + (2 * m + 1) * 32 * kPart);
+                r.get(y);
+#pragma unroll
+                for (int e = 0; e < VP; ++e) x[m][VP + e] = y[e];
+            }
+            fetch((now + kAhead - 1) % kAhead);
+            now = (now + 1) % kAhead;
+            if (w) {
 #pragma unroll
                 for (int m = 0; m < MU; ++m)
 #pragma unroll
-                    for (int e = 0; e < VP; ++e) amax = fmaxf(amax, fmaxf(fabsf(xa[m][e]), fabsf(xb[m][e])));
+                    for (int e = 0; e < 2 * VP; ++e) sum = fmaf(x[m][e], x[m][e], sum);
 #pragma unroll
-                for (int x = 16; x > 0; x >>= 1)
-                    if (x < lpr) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, x));
-                // (a row of tiny values keeps a normal scale, so that 0 / scale is 0)
-                const float scale = amax > 0.f ? fmaxf(amax / 448.f, 1.17549435e-38f) : 1.f;
+                for (int d = 16; d > 0; d >>= 1)
+                    if (d < lpr) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            }
+            if (kind != 2) {
+                const float f = w ? rsqrtf(fmaf(sum, a.inv_d, a.eps)) : 1.f;
+#pragma unroll
+                for (int m = 0; m < MU; ++m) {
+#pragma unroll
+                    for (int e = 0; e < VP; ++e) {
+                        float &x0 = x[m][IL ? 2 * e : e], &x1 = x[m][IL ? 2 * e + 1 : VP + e];
+                        float p = x0 * ac[m][e], q = x1 * bc[m][e];
+                        if (turns[m]) {       // (an element that does not turn never meets its partner)
+                            p = fmaf(-x1, bs[m][e], p);
+                            q = fmaf(x0, as[m][e], q);
+                        }
+                        x0 = p * f;
+                        x1 = q * f;
+                    }
+                }
+            }
+            float ya[MU][VP], yb[MU][VP];
+#pragma unroll
+            for (int m = 0; m < MU; ++m)
+#pragma unroll
+                for (int e = 0; e < VP; ++e) ya[m][e] = x[m][e], yb[m][e] = x[m][VP + e];
+            if (out) {
                 if (on) {
 #pragma unroll
                     for (int m = 0; m < MU; ++m) {
                         if (mine[m]) {
-                            store_e4m3<VP>(row + ia[m] / E, xa[m], scale);
-                            store_e4m3<VP>(row + ib[m] / E, xb[m], scale);
+                            store_n<T, VP>(out + ia[m], ya[m]);
+                            store_n<T, VP>(out + ib[m], yb[m]);
                         }
                     }
-                    if (lane == 0) (kind == 1 ? a.cache.ks : a.cache.vs)[slot * a.cache.Hkv + h] = scale;
                 }
+                out += step;
+            }
+            if (cache) {
+                if (a.append == 1) {
+                    if (on) {
+#pragma unroll
+                        for (int m = 0; m < MU; ++m) {
+                            if (mine[m]) {
+                                store_n<T, VP>(cache + ia[m], ya[m]);
+                                store_n<T, VP>(cache + ib[m], yb[m]);
+                            }
+                        }
+                    }
+                } else {
+                    float amax = 0.f;
+#pragma unroll
+                    for (int m = 0; m < MU; ++m)
+#pragma unroll
+                        for (int e = 0; e < 2 * VP; ++e) amax = fmaxf(amax, fabsf(x[m][e]));
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1)
+                        if (d < lpr) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+                    // (a row of tiny values keeps a normal scale, so that 0 / scale is 0)
+                    const float scale = amax > 0.f ? fmaxf(amax / 448.f, 1.17549435e-38f) : 1.f;
+                    if (on) {
+#pragma unroll
+                        for (int m = 0; m < MU; ++m) {
+                            if (mine[m]) {
+                                store_e4m3<VP>(cache + ia[m] / E, ya[m], scale);
+                                store_e4m3<VP>(cache + ib[m] / E, yb[m], scale);
+                            }
+                        }
+                        if (lane == 0) (kind == 1 ? a.cache.ks : a.cache.vs)[slot * a.cache.Hkv + h] = scale;
+                    }
+                }
+                cache += int64_t(groups) * a.cache.head_stride;
             }
         }
+        first = last;
+        ++kind;
+        h = group;
+        heads = a.Hkv;
     }
 }
 
-template <typename T, int VP, int LPR>
-lsa_status launch_as(const QkArgs &a, unsigned grid, size_t smem, cudaStream_t st) {
-    LSA_CUDA(ensure_smem(qk_norm_rope<T, VP, LPR>, smem));
-    LSA_CUDA(launch_pdl(qk_norm_rope<T, VP, LPR>, dim3(grid), dim3(kThreads), smem, st, a));
+template <typename T, int VP, int MU, int LPR>
+lsa_status launch_as(const QkArgs &a, unsigned grid, cudaStream_t st) {
+    const size_t smem = size_t(kWarps) * (size_t(kAhead) * 32 * 2 * MU * VP * sizeof(T) + size_t(a.rot / 2) * 8);
+    auto *kernel = a.interleaved ? qk_norm_rope<T, VP, MU, LPR, true> : qk_norm_rope<T, VP, MU, LPR, false>;
+    LSA_CUDA(ensure_smem(kernel, smem));
+    LSA_CUDA(launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, st, a));
     LSA_LAUNCHED("qk_norm_rope");
     return LSA_OK;
 }
 // The usual head dims have the lanes of a row at compile time (64, 128 and 256 elements at the widest unit).
 template <typename T, int VP>
-lsa_status launch_vp(const QkArgs &a, unsigned grid, size_t smem, cudaStream_t st) {
+lsa_status launch_vp(const QkArgs &a, unsigned grid, cudaStream_t st) {
+    const int units = (a.D / 2 / VP + a.lpr - 1) / a.lpr;    // of a lane: at most 8 / VP
     if constexpr (VP * sizeof(T) == 16) {
         constexpr int kRow = 128 / 2 / VP;
-        if (a.lpr == kRow / 2) return launch_as<T, VP, kRow / 2>(a, grid, smem, st);
-        if (a.lpr == kRow) return launch_as<T, VP, kRow>(a, grid, smem, st);
-        if (a.lpr == 2 * kRow) return launch_as<T, VP, 2 * kRow>(a, grid, smem, st);
+        if (a.lpr == kRow / 2) return launch_as<T, VP, 1, kRow / 2>(a, grid, st);
+        if (a.lpr == kRow) return launch_as<T, VP, 1, kRow>(a, grid, st);
+        if (a.lpr == 2 * kRow && units == 1) return launch_as<T, VP, 1, 2 * kRow>(a, grid, st);
     }
-    return launch_as<T, VP, 0>(a, grid, smem, st);
+    if (units == 1) return launch_as<T, VP, 1, 0>(a, grid, st);
+    if constexpr (VP <= 1)
+        if (units > 4) return launch_as<T, VP, 8, 0>(a, grid, st);
+    if constexpr (VP <= 2)
+        if (units > 2) return launch_as<T, VP, 4, 0>(a, grid, st);
+    if constexpr (VP <= 4) return launch_as<T, VP, 2, 0>(a, grid, st);
+    return launch_as<T, VP, 1, 0>(a, grid, st);
 }
 
 }  // namespace
@@ -451,6 +503,7 @@ extern "C" lsa_status lsa_qk_norm_rope(const void *q, int64_t q_stride, void *q_
     a.sign = rope && rope->inverse ? -1.f : 1.f;
     a.mscale = rope && rope->mscale != 0.f ? rope->mscale : 1.f;
     a.eps = eps;
+    a.inv_d = 1.f / float(D);
     a.wq = static_cast<const uint8_t *>(q_weight);
     a.wk = static_cast<const uint8_t *>(k_weight);
     a.pos = pos;
@@ -472,27 +525,29 @@ extern "C" lsa_status lsa_qk_norm_rope(const void *q, int64_t q_stride, void *q_
     a.nq = (Hq + groups - 1) / groups;
     a.nk = (a.Hkv + groups - 1) / groups;
     a.nv = v ? a.nk : 0;
-    // a warp a token, or several until the device has warps enough (16 an SM)
+    // a warp a token; several, each with its own angles, while tokens are fewer than the device's warps (16 an SM), or
+    // while that leaves each ten rounds and the warps are fewer than four times that, so that the last ones leave no SM
+    // idle for long (4099 tokens of 65 rows of 128: 70 us with one warp a token, 64 with three; 8192 tokens of 17 rows of
+    // 512: 57 us with one, 81 with four)
     const int rounds = a.nq + a.nk + a.nv;
-    const int64_t want = int64_t(sm_count()) * 16 / T;
-    a.parts = int32_t(want < 1 ? 1 : want < rounds ? want : rounds);
+    const int64_t fill = int64_t(sm_count()) * 16;
+    a.parts = int32_t(fill / T < 1 ? 1 : fill / T < rounds ? fill / T : rounds);
+    while (T * a.parts < 4 * fill && rounds / (a.parts + 1) >= 10) ++a.parts;
     const int64_t items = T * a.parts;
-    constexpr int kWarps = kThreads / 32;
     const unsigned grid = unsigned((items + kWarps - 1) / kWarps);
-    const size_t smem = size_t(kWarps) * (rot / 2) * 8;
     cudaStream_t st = as_stream(stream);
     if (dtype == LSA_BF16) {
         switch (vp) {
-        case 8: return launch_vp<uint16_t, 8>(a, grid, smem, st);
-        case 4: return launch_vp<uint16_t, 4>(a, grid, smem, st);
-        case 2: return launch_vp<uint16_t, 2>(a, grid, smem, st);
-        default: return launch_vp<uint16_t, 1>(a, grid, smem, st);
+        case 8: return launch_vp<uint16_t, 8>(a, grid, st);
+        case 4: return launch_vp<uint16_t, 4>(a, grid, st);
+        case 2: return launch_vp<uint16_t, 2>(a, grid, st);
+        default: return launch_vp<uint16_t, 1>(a, grid, st);
         }
     }
     switch (vp) {
-    case 4: return launch_vp<float, 4>(a, grid, smem, st);
-    case 2: return launch_vp<float, 2>(a, grid, smem, st);
-    default: return launch_vp<float, 1>(a, grid, smem, st);
+    case 4: return launch_vp<float, 4>(a, grid, st);
+    case 2: return launch_vp<float, 2>(a, grid, st);
+    default: return launch_vp<float, 1>(a, grid, st);
     }
 }
 
