@@ -22,6 +22,13 @@ inline CacheView view_of(const lsa_page_cache &c) {
                      c.page_size, c.Hkv, c.D};
 }
 
+// a / b for a, b >= 0.  Counts of work fit 32 bits in all but the largest calls, and a 64-bit division is a hundred
+// instructions that every CTA would fetch before its first load.
+__device__ __noinline__ inline int64_t div64(int64_t a, int64_t b) { return a / b; }
+__device__ __forceinline__ int64_t div_units(int64_t a, int64_t b) {
+    return uint64_t(a | b) >> 32 ? div64(a, b) : int64_t(uint32_t(a) / uint32_t(b));
+}
+
 // Validates a cache descriptor on the host (`who`: the entry point, for the message).
 lsa_status check_cache(const lsa_page_cache *c, const char *who);
 

@@ -76,13 +76,6 @@ __device__ __forceinline__ int32_t units_of(const AttnArgs &a, int b) {
     return n ? n + a.lead : 0;
 }
 
-// a / b for a, b >= 0.  Unit counts fit 32 bits in all but the largest calls, and a 64-bit division is a hundred
-// instructions that every CTA would fetch before its first load.
-__device__ __noinline__ inline int64_t div64(int64_t a, int64_t b) { return a / b; }
-__device__ __forceinline__ int64_t div_units(int64_t a, int64_t b) {
-    return uint64_t(a | b) >> 32 ? div64(a, b) : int64_t(uint32_t(a) / uint32_t(b));
-}
-
 // Where a unit lies: sequence b, whose first unit is `base`.
 struct Where {
     int64_t total, share;   // units of the call, units of a CTA

@@ -4,7 +4,8 @@
 // written to q_out / k_out and, with the values, to the slots of a paged cache.
 //
 // One pass: a row is read once and written once, so the call is bound by HBM for many tokens and by its latency for
-// few.  A warp does the rows of one token (or a part of them, where tokens are few), LPR lanes a row.  A lane owns units
+// few.  A warp does rows of one token after the other, LPR lanes a row; the device's warps share all rows evenly, whatever
+// the number of tokens (a warp a token left SMs idle at the end: 65 us against 52 for 4099 tokens of 65 rows).  A lane owns units
 // of VP pairs of the row, i.e. VP elements of the rotated part's first half and the VP that pair with them (or 2 VP
 // neighbours where pairs are interleaved), so rotating needs no exchange between lanes and both accesses are as wide as
 // the sizes allow (16 bytes at VP = 8 bf16 or 4 fp32).  As a lane's pairs are the same in every row, the products of its
@@ -48,7 +49,8 @@ struct QkArgs {
     int32_t *err;
     int32_t lpr;                 // lanes of a row, a power of two
     int32_t nq, nk, nv;          // rounds of a token's queries, keys, values: 32 / lpr rows each
-    int32_t parts;               // warps of a token
+    int64_t share, spare;        // rounds of a warp; the first `spare` warps have one more
+    int64_t warps;
 };
 
 // N consecutive elements as they lie in memory, and in fp32.
@@ -140,10 +142,12 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(QkArgs a) {
     extern __shared__ __align__(16) uint8_t smem[];   // [warps] rings of kAhead rounds, then the angles [warps][rot / 2]
     const int lpr = LPR ? LPR : a.lpr, half = a.rot / 2, U = a.D / 2 / VP, rest = (a.D - a.rot) / 2;
     const int wl = threadIdx.x & 31, lane = wl & (lpr - 1), group = wl / lpr, groups = 32 / lpr;
-    const uint32_t item = blockIdx.x * kWarps + (threadIdx.x >> 5), token = item / uint32_t(a.parts);
-    const int64_t tok = token;
-    const int part = int(item - token * a.parts), rounds = a.nq + a.nk + a.nv;
-    const int begin = a.parts == 1 ? 0 : part * rounds / a.parts, end = a.parts == 1 ? rounds : (part + 1) * rounds / a.parts;
+    const int64_t self = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const int rounds = a.nq + a.nk + a.nv;
+    int64_t left = self < a.warps ? a.share + (self < a.spare) : 0;       // rounds still to compute
+    const int64_t start = self * a.share + (self < a.spare ? self : a.spare);
+    int64_t tok = paged::div_units(start, rounds);
+    int rd = int(start - tok * rounds);
 
     int ia[MU], ib[MU];      // byte offset of a unit's first and second part
     bool mine[MU], turns[MU];
@@ -162,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(QkArgs a) {
     }
     pdl_launch_dependents();
     pdl_wait();
-    if (tok >= a.T) return;
+    if (left == 0) return;
     // the token's rounds are its queries' (kind 0), keys' and values', `groups` rows each; the next rounds' elements are on
     // their way while one is computed (a lane without a unit keeps zeros in the ring, a row that is not there what was there
     // before, and neither is stored)
@@ -177,19 +181,28 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(QkArgs a) {
                 }
         }
     }
-    auto source = [&](int kind, int h) {
+    auto source = [&](int64_t tok, int kind, int h) {
         return (kind == 0 ? a.q + tok * a.q_stride : kind == 1 ? a.k + tok * a.k_stride : a.v + tok * a.v_stride) +
                int64_t(h) * a.row_bytes;
     };
     const int step = groups * a.row_bytes;
-    int rd = begin, kind = begin < a.nq ? 0 : begin < a.nq + a.nk ? 1 : 2;
+    int kind = rd < a.nq ? 0 : rd < a.nq + a.nk ? 1 : 2;
     int first = kind == 0 ? 0 : kind == 1 ? a.nq : a.nq + a.nk;            // the kind's first round
-    int h = (rd - first) * groups + group, heads = kind == 0 ? a.Hq : a.Hkv;
-    // the fetching side's place
-    int f_rd = begin, f_kind = kind, f_h = h, f_last = first + (kind == 0 ? a.nq : kind == 1 ? a.nk : a.nv);
-    const uint8_t *src = source(kind, h);
+    int h = (rd - first) * groups + group;
+    // the fetching side's place, and what a token needs besides its rows, asked for a token ahead
+    int64_t f_tok = tok, f_left = left;
+    int f_rd = rd, f_kind = kind, f_h = h, f_last = first + (kind == 0 ? a.nq : kind == 1 ? a.nk : a.nv);
+    const uint8_t *src = source(tok, kind, h);
+    int32_t n_pos = 0, n_row = 0, n_at = -1;
+    auto meet = [&](int64_t t) {
+        if (half) n_pos = a.pos[t];
+        if (a.append) {
+            n_row = a.seq ? a.seq[t] : int32_t(t);
+            n_at = a.at[t];
+        }
+    };
     auto fetch = [&](int slot) {
-        if (f_rd < end) {
+        if (f_left > 0) {
             if (f_h < (f_kind == 0 ? a.Hq : a.Hkv)) {
 #pragma unroll
                 for (int m = 0; m < MU; ++m) {
@@ -201,188 +214,205 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(QkArgs a) {
             }
             f_h += groups;
             src += step;
-            if (++f_rd == f_last) {
-                ++f_kind;
+            --f_left;
+            if (++f_rd == f_last && f_left > 0) {
                 f_h = group;
-                f_last += f_kind == 1 ? a.nk : a.nv;
-                if (f_rd < end) src = source(f_kind, group);
+                if (f_rd == rounds) {
+                    f_rd = 0;
+                    f_kind = 0;
+                    f_last = a.nq;
+                    ++f_tok;
+                } else {
+                    ++f_kind;
+                    f_last += f_kind == 1 ? a.nk : a.nv;
+                }
+                src = source(f_tok, f_kind, group);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    meet(tok);
     for (int s = 0; s < kAhead - 1; ++s) fetch(s);
     int now = 0;
+    float2 *cs = reinterpret_cast<float2 *>(smem + kWarps * kAhead * kSlot) + (threadIdx.x >> 5) * half;
 
-    // where the token goes in the cache (every lane finds it)
-    int64_t off = -1, slot = 0;
-    if (a.append && end > a.nq) {
-        const int64_t row = a.seq ? a.seq[tok] : tok, at = a.at[tok];
-        if (row >= 0 && at >= 0) {
+    while (left > 0) {
+        // ---- a token: where it goes in the cache (every lane finds it), and its angles
+        const int32_t pos = n_pos;
+        const int end = int(left < rounds - rd ? rd + left : rounds), begun = rd;
+        int64_t off = -1, slot = 0;
+        if (a.append && end > a.nq && n_row >= 0 && n_at >= 0) {
             int64_t page = -1;
-            const int s = row < a.n_rows && at < a.reach ? int(uint32_t(at) % uint32_t(a.cache.page_size)) : 0;
-            if (row < a.n_rows && at < a.reach) page = a.table[row * a.table_stride + uint32_t(at) / uint32_t(a.cache.page_size)];
+            const uint32_t size = a.cache.page_size, p = uint32_t(n_at) / size, s = uint32_t(n_at) - p * size;
+            if (n_row < a.n_rows && n_at < a.reach) page = a.table[n_row * a.table_stride + p];
             if (page >= 0 && page < a.cache.n_pages) {
-                off = page * a.cache.page_stride + s * a.cache.slot_stride;
-                slot = page * a.cache.page_size + s;
+                off = page * a.cache.page_stride + int64_t(s) * a.cache.slot_stride;
+                slot = page * size + s;
             } else if (wl == 0) {
                 raise_err(a.err, LSA_ERR_INVALID);
             }
         }
-    }
-    float2 *cs = reinterpret_cast<float2 *>(smem + kWarps * kAhead * kSlot) + (threadIdx.x >> 5) * half;
-    if (begin < a.nq + a.nk) {
-        for (int i = wl; i < half; i += 32) {
-            const double turn = double(a.pos[tok]) * a.freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
-            float s, c;
-            sincospif(float(2.0 * (turn - rint(turn))), &s, &c);
-            cs[i] = make_float2(a.mscale * c, a.mscale * a.sign * s);
+        if (left > end - rd) meet(tok + 1);      // (used when the next token's turn comes)
+        if (rd < a.nq + a.nk) {
+            __syncwarp();           // (the token before has read its angles)
+            for (int i = wl; i < half; i += 32) {
+                const double turn = double(pos) * a.freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
+                float s, c;
+                sincospif(float(2.0 * (turn - rint(turn))), &s, &c);
+                cs[i] = make_float2(a.mscale * c, a.mscale * a.sign * s);
+            }
+            __syncwarp();
         }
-        __syncwarp();
-    }
 
-    float ac[MU][VP], as[MU][VP], bc[MU][VP], bs[MU][VP];   // weights times cos and sin, of a unit's two parts
-    while (rd < end) {
-        const int last = min(end, first + (kind == 0 ? a.nq : kind == 1 ? a.nk : a.nv));
-        const uint8_t *w = kind == 0 ? a.wq : kind == 1 ? a.wk : nullptr;
-        uint8_t *out = kind == 0 ? a.q_out + tok * a.q_out_stride
-                                 : kind == 1 && a.k_out ? a.k_out + tok * a.k_out_stride : nullptr;
-        if (out) out += int64_t(h) * a.row_bytes;
-        uint8_t *cache = kind != 0 && off >= 0 ? (kind == 1 ? a.cache.k : a.cache.v) + off + h * a.cache.head_stride : nullptr;
-        if (kind != 2) {
-#pragma unroll
-            for (int m = 0; m < MU; ++m) {
-                float wt[2 * VP];        // of the unit's elements, in the order of the row where pairs are neighbours
-                if (w && mine[m]) {
-                    float y[VP];
-                    Raw<T, VP> x;
-                    x.load(w + ia[m]);
-                    x.get(y);
-#pragma unroll
-                    for (int e = 0; e < VP; ++e) wt[e] = y[e];
-                    x.load(w + ib[m]);
-                    x.get(y);
-#pragma unroll
-                    for (int e = 0; e < VP; ++e) wt[VP + e] = y[e];
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 2 * VP; ++e) wt[e] = 1.f;
-                }
-#pragma unroll
-                for (int e = 0; e < VP; ++e) {
-                    const float2 c = turns[m] ? cs[(lane + lpr * m) * VP + e] : make_float2(1.f, 0.f);
-                    const float u = IL ? wt[2 * e] : wt[e], v = IL ? wt[2 * e + 1] : wt[VP + e];
-                    ac[m][e] = u * c.x;
-                    as[m][e] = u * c.y;
-                    bc[m][e] = v * c.x;
-                    bs[m][e] = v * c.y;
-                }
-            }
-        }
-#pragma unroll 1
-        for (; rd < last; ++rd, h += groups) {
-            const bool on = h < heads;
-            float x[MU][2 * VP];         // the unit's first part, then its second
-            float sum = 0.f;
-            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 2) : "memory");
-            const uint8_t *at = ring + now * kSlot;
-#pragma unroll
-            for (int m = 0; m < MU; ++m) {
-                float y[VP];
-                Raw<T, VP> r;
-                r.load(at + 2 * m * 32 * kPart);
-                r.get(y);
-#pragma unroll
-                for (int e = 0; e < VP; ++e) x[m][e] = y[e];
-                r.load(at + (2 * m + 1) * 32 * kPart);
-                r.get(y);
-#pragma unroll
-                for (int e = 0; e < VP; ++e) x[m][VP + e] = y[e];
-            }
-            fetch((now + kAhead - 1) % kAhead);
-            now = (now + 1) % kAhead;
-            if (w) {
-#pragma unroll
-                for (int m = 0; m < MU; ++m)
-#pragma unroll
-                    for (int e = 0; e < 2 * VP; ++e) sum = fmaf(x[m][e], x[m][e], sum);
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1)
-                    if (d < lpr) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            }
+        float ac[MU][VP], as[MU][VP], bc[MU][VP], bs[MU][VP];   // weights times cos and sin, of a unit's two parts
+        while (rd < end) {
+            const int heads = kind == 0 ? a.Hq : a.Hkv;
+            const int last = min(end, first + (kind == 0 ? a.nq : kind == 1 ? a.nk : a.nv));
+            const uint8_t *w = kind == 0 ? a.wq : kind == 1 ? a.wk : nullptr;
+            uint8_t *out = kind == 0 ? a.q_out + tok * a.q_out_stride
+                                     : kind == 1 && a.k_out ? a.k_out + tok * a.k_out_stride : nullptr;
+            if (out) out += int64_t(h) * a.row_bytes;
+            uint8_t *cache = kind != 0 && off >= 0 ? (kind == 1 ? a.cache.k : a.cache.v) + off + h * a.cache.head_stride : nullptr;
             if (kind != 2) {
-                const float f = w ? rsqrtf(fmaf(sum, a.inv_d, a.eps)) : 1.f;
 #pragma unroll
                 for (int m = 0; m < MU; ++m) {
+                    float wt[2 * VP];        // of the unit's elements, in the order of the row where pairs are neighbours
+                    if (w && mine[m]) {
+                        float y[VP];
+                        Raw<T, VP> x;
+                        x.load(w + ia[m]);
+                        x.get(y);
+#pragma unroll
+                        for (int e = 0; e < VP; ++e) wt[e] = y[e];
+                        x.load(w + ib[m]);
+                        x.get(y);
+#pragma unroll
+                        for (int e = 0; e < VP; ++e) wt[VP + e] = y[e];
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 2 * VP; ++e) wt[e] = 1.f;
+                    }
 #pragma unroll
                     for (int e = 0; e < VP; ++e) {
-                        float &x0 = x[m][IL ? 2 * e : e], &x1 = x[m][IL ? 2 * e + 1 : VP + e];
-                        float p = x0 * ac[m][e], q = x1 * bc[m][e];
-                        if (turns[m]) {       // (an element that does not turn never meets its partner)
-                            p = fmaf(-x1, bs[m][e], p);
-                            q = fmaf(x0, as[m][e], q);
-                        }
-                        x0 = p * f;
-                        x1 = q * f;
+                        const float2 c = turns[m] ? cs[(lane + lpr * m) * VP + e] : make_float2(1.f, 0.f);
+                        const float u = IL ? wt[2 * e] : wt[e], v = IL ? wt[2 * e + 1] : wt[VP + e];
+                        ac[m][e] = u * c.x;
+                        as[m][e] = u * c.y;
+                        bc[m][e] = v * c.x;
+                        bs[m][e] = v * c.y;
                     }
                 }
             }
-            float ya[MU][VP], yb[MU][VP];
+#pragma unroll 1
+            for (; rd < last; ++rd, h += groups) {
+                const bool on = h < heads;
+                float x[MU][2 * VP];         // the unit's first part, then its second
+                float sum = 0.f;
+                asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 2) : "memory");
+                const uint8_t *at = ring + now * kSlot;
 #pragma unroll
-            for (int m = 0; m < MU; ++m)
+                for (int m = 0; m < MU; ++m) {
+                    float y[VP];
+                    Raw<T, VP> r;
+                    r.load(at + 2 * m * 32 * kPart);
+                    r.get(y);
 #pragma unroll
-                for (int e = 0; e < VP; ++e) ya[m][e] = x[m][e], yb[m][e] = x[m][VP + e];
-            if (out) {
-                if (on) {
+                    for (int e = 0; e < VP; ++e) x[m][e] = y[e];
+                    r.load(at + (2 * m + 1) * 32 * kPart);
+                    r.get(y);
 #pragma unroll
-                    for (int m = 0; m < MU; ++m) {
-                        if (mine[m]) {
-                            store_n<T, VP>(out + ia[m], ya[m]);
-                            store_n<T, VP>(out + ib[m], yb[m]);
-                        }
-                    }
+                    for (int e = 0; e < VP; ++e) x[m][VP + e] = y[e];
                 }
-                out += step;
-            }
-            if (cache) {
-                if (a.append == 1) {
-                    if (on) {
-#pragma unroll
-                        for (int m = 0; m < MU; ++m) {
-                            if (mine[m]) {
-                                store_n<T, VP>(cache + ia[m], ya[m]);
-                                store_n<T, VP>(cache + ib[m], yb[m]);
-                            }
-                        }
-                    }
-                } else {
-                    float amax = 0.f;
+                fetch((now + kAhead - 1) % kAhead);
+                now = (now + 1) % kAhead;
+                if (w) {
 #pragma unroll
                     for (int m = 0; m < MU; ++m)
 #pragma unroll
-                        for (int e = 0; e < 2 * VP; ++e) amax = fmaxf(amax, fabsf(x[m][e]));
+                        for (int e = 0; e < 2 * VP; ++e) sum = fmaf(x[m][e], x[m][e], sum);
 #pragma unroll
                     for (int d = 16; d > 0; d >>= 1)
-                        if (d < lpr) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-                    // (a row of tiny values keeps a normal scale, so that 0 / scale is 0)
-                    const float scale = amax > 0.f ? fmaxf(amax / 448.f, 1.17549435e-38f) : 1.f;
+                        if (d < lpr) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                }
+                if (kind != 2) {
+                    const float f = w ? rsqrtf(fmaf(sum, a.inv_d, a.eps)) : 1.f;
+#pragma unroll
+                    for (int m = 0; m < MU; ++m) {
+#pragma unroll
+                        for (int e = 0; e < VP; ++e) {
+                            float &x0 = x[m][IL ? 2 * e : e], &x1 = x[m][IL ? 2 * e + 1 : VP + e];
+                            float p = x0 * ac[m][e], q = x1 * bc[m][e];
+                            if (turns[m]) {       // (an element that does not turn never meets its partner)
+                                p = fmaf(-x1, bs[m][e], p);
+                                q = fmaf(x0, as[m][e], q);
+                            }
+                            x0 = p * f;
+                            x1 = q * f;
+                        }
+                    }
+                }
+                float ya[MU][VP], yb[MU][VP];
+#pragma unroll
+                for (int m = 0; m < MU; ++m)
+#pragma unroll
+                    for (int e = 0; e < VP; ++e) ya[m][e] = x[m][e], yb[m][e] = x[m][VP + e];
+                if (out) {
                     if (on) {
 #pragma unroll
                         for (int m = 0; m < MU; ++m) {
                             if (mine[m]) {
-                                store_e4m3<VP>(cache + ia[m] / E, ya[m], scale);
-                                store_e4m3<VP>(cache + ib[m] / E, yb[m], scale);
+                                store_n<T, VP>(out + ia[m], ya[m]);
+                                store_n<T, VP>(out + ib[m], yb[m]);
                             }
                         }
-                        if (lane == 0) (kind == 1 ? a.cache.ks : a.cache.vs)[slot * a.cache.Hkv + h] = scale;
                     }
+                    out += step;
                 }
-                cache += int64_t(groups) * a.cache.head_stride;
+                if (cache) {
+                    if (a.append == 1) {
+                        if (on) {
+#pragma unroll
+                            for (int m = 0; m < MU; ++m) {
+                                if (mine[m]) {
+                                    store_n<T, VP>(cache + ia[m], ya[m]);
+                                    store_n<T, VP>(cache + ib[m], yb[m]);
+                                }
+                            }
+                        }
+                    } else {
+                        float amax = 0.f;
+#pragma unroll
+                        for (int m = 0; m < MU; ++m)
+#pragma unroll
+                            for (int e = 0; e < 2 * VP; ++e) amax = fmaxf(amax, fabsf(x[m][e]));
+#pragma unroll
+                        for (int d = 16; d > 0; d >>= 1)
+                            if (d < lpr) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+                        // (a row of tiny values keeps a normal scale, so that 0 / scale is 0)
+                        const float scale = amax > 0.f ? fmaxf(amax / 448.f, 1.17549435e-38f) : 1.f;
+                        if (on) {
+#pragma unroll
+                            for (int m = 0; m < MU; ++m) {
+                                if (mine[m]) {
+                                    store_e4m3<VP>(cache + ia[m] / E, ya[m], scale);
+                                    store_e4m3<VP>(cache + ib[m] / E, yb[m], scale);
+                                }
+                            }
+                            if (lane == 0) (kind == 1 ? a.cache.ks : a.cache.vs)[slot * a.cache.Hkv + h] = scale;
+                        }
+                    }
+                    cache += int64_t(groups) * a.cache.head_stride;
+                }
             }
+            first = last;
+            ++kind;
+            h = group;
         }
-        first = last;
-        ++kind;
+        // ---- the next token
+        left -= end - begun;
+        ++tok;
+        rd = first = kind = 0;
         h = group;
-        heads = a.Hkv;
     }
 }
 
@@ -525,16 +555,13 @@ extern "C" lsa_status lsa_qk_norm_rope(const void *q, int64_t q_stride, void *q_
     a.nq = (Hq + groups - 1) / groups;
     a.nk = (a.Hkv + groups - 1) / groups;
     a.nv = v ? a.nk : 0;
-    // a warp a token; several, each with its own angles, while tokens are fewer than the device's warps (16 an SM), or
-    // while that leaves each ten rounds and the warps are fewer than four times that, so that the last ones leave no SM
-    // idle for long (4099 tokens of 65 rows of 128: 70 us with one warp a token, 64 with three; 8192 tokens of 17 rows of
-    // 512: 57 us with one, 81 with four)
+    // every warp takes the same number of rounds, through the ends of tokens: 16 warps an SM, all resident at once
     const int rounds = a.nq + a.nk + a.nv;
-    const int64_t fill = int64_t(sm_count()) * 16;
-    a.parts = int32_t(fill / T < 1 ? 1 : fill / T < rounds ? fill / T : rounds);
-    while (T * a.parts < 4 * fill && rounds / (a.parts + 1) >= 10) ++a.parts;
-    const int64_t items = T * a.parts;
-    const unsigned grid = unsigned((items + kWarps - 1) / kWarps);
+    const int64_t total = T * rounds, most = int64_t(sm_count()) * 16;
+    a.warps = total < most ? total : most;
+    a.share = total / a.warps;
+    a.spare = total - a.share * a.warps;
+    const unsigned grid = unsigned((a.warps + kWarps - 1) / kWarps);
     cudaStream_t st = as_stream(stream);
     if (dtype == LSA_BF16) {
         switch (vp) {
