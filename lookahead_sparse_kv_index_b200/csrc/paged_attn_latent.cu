@@ -12,8 +12,8 @@
 //   * P enters as two bf16 numbers (a weight and what its rounding left), as in paged_attn_mma.cu.
 // Tensor memory: O in columns 0 .. 255, two buffers of S in 256 .. 383, Q_r (bf16, the MMA's A operand) in 384 .. 511;
 // Q there leaves shared memory to four tiles of rows (32 KB each), P (2 x 16 KB) and two buffers of the other's S.
-// Sixteen warps: 0-7 softmax (thread = head, half of the tile's entries), 8-11 send S_r, 12 issues the MMAs, 13-14 copy
-// rows (cp.async), 15 tells the other CTA what was read of its scores.  Sending and telling have warps of their own
+// Sixteen warps: 0-7 softmax (thread = head, half of the tile's entries), 8-11 send S_r, 12 issues the MMAs, 13-14 load
+// rows (TMA or cp.async), 15 tells the other CTA what was read of its scores.  Sending and telling have warps of their own
 // because they are slow and nothing depends on them at once: the 32 KB of a tile cross in about 1300 cycles, and a
 // release at cluster scope takes 350.
 // A tile passes load, S, exchange, softmax, P V; what counts is that these overlap.  S of tile i + 2 is issued as soon as
@@ -21,6 +21,8 @@
 // S of tile i + 1 issued after P V of tile i - 1 the softmax and the tensor pipe took turns: 423 us for 128 heads over
 // 4 x 131072 entries).  The running max is a reference that moves, and O is rescaled, only when a score passes it by 2^8;
 // a barrier that every tile needs anyway tells whether one did.  Every wait is bounded; the two CTAs leave together.
+#include <cuda.h>
+
 #include "paged_attn.cuh"
 #include "tc_ptx.cuh"
 
@@ -158,8 +160,18 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// 4-D tiled TMA load into shared memory of this CTA, completion counted on `bar`.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z, int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::
+            "r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
+// rows_map: the cache as [page][slot][head][element]; box: rows of a TMA load, 0 for none.
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-paged_attn_latent(AttnArgs a) {
+paged_attn_latent(const __grid_constant__ CUtensorMap rows_map, AttnArgs a, int box) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *kvs = smem, *ps = kvs + kStages * kStageBytes, *recv = ps + 2 * kPBytes;
@@ -226,7 +238,11 @@ paged_attn_latent(AttnArgs a) {
             }
         } else if (warp >= kLoadWarp) {
             // ---- rows: lane l of warp w places row 32 w + l (entry t, slot s of the sequence's page p; the page's index is
-            // read a tile ahead), then eight lanes copy a row, 16 bytes each of its four 128-byte blocks
+            // read a tile ahead).  Where `box` rows of the tile always lie side by side in a page, one lane of each `box`
+            // loads them by TMA, a 64-column block a time (a box of a page that is not there loads zeros: its index is
+            // past the cache's end).  Else, and in a piece's last tile, whose entries may end inside a box, eight lanes
+            // copy a row, 16 bytes each of its four 128-byte blocks.
+            const bool boxes = box > 0 && lo % box == 0;
             const int w = warp - kLoadWarp, lr = lane >> 3, lp = lane & 7;
             const int32_t *row = a.table + int64_t(b) * a.table_stride;
             const uint8_t *base = a.cache.k + kvh * a.cache.head_stride + rank * (kCols * 2) + lp * 16;
@@ -242,6 +258,8 @@ paged_attn_latent(AttnArgs a) {
                     else
                         raise_err(a.err, LSA_ERR_INVALID);
                 }
+                const int64_t now_page = page;
+                const int now_slot = s_in;
                 t += kTile;
                 p += hop_p;
                 s_in += hop_s;
@@ -250,20 +268,34 @@ paged_attn_latent(AttnArgs a) {
                     ++p;
                 }
                 page = t < hi ? row[p] : -1;
-                if (g >= kStages && !mbar_wait(&bars.kv_free[s], (g / kStages - 1) & 1, abort_v, kWaitLimitNs)) break;
+                const bool waited = g < kStages || mbar_wait(&bars.kv_free[s], (g / kStages - 1) & 1, abort_v, kWaitLimitNs);
+                if (!__all_sync(0xffffffffu, waited)) break;
                 const uint32_t mask = __ballot_sync(0xffffffffu, off >= 0);
                 const uint32_t dst = smem_u32(kvs) + s * kStageBytes;
+                if (boxes && lo + (j + 1) * kTile <= hi) {
+                    if (lane == 0) mbar_arrive_expect_tx(&bars.kv_full[s], kStageBytes / kLoadWarps);
+                    else mbar_arrive(&bars.kv_full[s]);
+                    if (lane % box == 0) {
+                        const int pg = off >= 0 ? int(now_page) : int(a.cache.n_pages);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int r = 32 * w + 4 * i + lr;
-                    const int64_t from = __shfl_sync(0xffffffffu, off, 4 * i + lr);
-                    const uint32_t bytes = from >= 0 ? 16u : 0u;
-                    const uint8_t *src = base + (from >= 0 ? from : 0);
-                    const uint32_t to = dst + r * 128 + ((lp ^ (r & 7)) << 4);
+                        for (int c = 0; c < 4; ++c)
+                            tma_load_4d(dst + c * kBlock + (32 * w + lane) * 128, &rows_map, &bars.kv_full[s],
+                                        int(rank) * kCols + c * 64, kvh, now_slot, pg);
+                    }
+                    __syncwarp();
+                } else {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) cp_async_16(to + c * kBlock, src + c * 128, bytes);
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = 32 * w + 4 * i + lr;
+                        const int64_t from = __shfl_sync(0xffffffffu, off, 4 * i + lr);
+                        const uint32_t bytes = from >= 0 ? 16u : 0u;
+                        const uint8_t *src = base + (from >= 0 ? from : 0);
+                        const uint32_t to = dst + r * 128 + ((lp ^ (r & 7)) << 4);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) cp_async_16(to + c * kBlock, src + c * 128, bytes);
+                    }
+                    cp_async_arrive_noinc(&bars.kv_full[s]);
                 }
-                cp_async_arrive_noinc(&bars.kv_full[s]);
                 if (lane == 0) {
                     s_mask[s][w] = mask;
                     mbar_arrive(&bars.mask_full[s]);
@@ -563,6 +595,24 @@ paged_attn_latent(AttnArgs a) {
             if (a.seq_len[b] > a.reach) raise_err(a.err, LSA_ERR_CAPACITY);
 }
 
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<EncodeTiledFn>(p);
+    }();
+    return fn;
+}
+
 }  // namespace
 
 bool latent_supported(const lsa_page_cache &c, int Hq) {
@@ -580,8 +630,29 @@ AttnPlan plan_latent(const lsa_page_cache &c, int Hq) {
 }
 
 lsa_status launch_latent(const AttnArgs &a, int grid, cudaStream_t st) {
+    // rows side by side in a page from any multiple of `box` entries on, at least the 8 of a swizzle atom
+    const int size = a.cache.page_size;
+    int box = size % 32 == 0 ? 32 : size % 16 == 0 ? 16 : size % 8 == 0 ? 8 : 0;
+    CUtensorMap rows_map = {};
+    if (box) {
+        EncodeTiledFn enc = encode_fn();
+        if (!enc) {
+            set_error("lsa_paged_attn: cuTensorMapEncodeTiled is unavailable");
+            return LSA_ERR_CUDA;
+        }
+        const cuuint32_t unit[4] = {1, 1, 1, 1}, extent[4] = {64, 1, cuuint32_t(box), 1};
+        const cuuint64_t dims[4] = {cuuint64_t(kD), cuuint64_t(a.cache.Hkv), cuuint64_t(size), cuuint64_t(a.cache.n_pages)};
+        const cuuint64_t row = kD * 2;
+        const cuuint64_t strides[3] = {a.cache.Hkv > 1 ? cuuint64_t(a.cache.head_stride) : row,
+                                       cuuint64_t(a.cache.slot_stride),
+                                       a.cache.n_pages > 1 ? cuuint64_t(a.cache.page_stride) : row};
+        const CUresult r = enc(&rows_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, a.cache.k, dims, strides, extent, unit,
+                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (r != CUDA_SUCCESS) box = 0;      // strides that a map cannot hold (2^40 bytes or more): the rows are copied
+    }
     LSA_CUDA(ensure_smem(paged_attn_latent, kSmem));
-    LSA_CUDA(launch_pdl(paged_attn_latent, dim3(2 * grid), dim3(kThreads), kSmem, st, a));
+    LSA_CUDA(launch_pdl(paged_attn_latent, dim3(2 * grid), dim3(kThreads), kSmem, st, rows_map, a, box));
     LSA_LAUNCHED("paged_attn_latent");
     return LSA_OK;
 }

@@ -154,6 +154,19 @@ def test_attention_latent_long(lsa, dtype, Hq, lens):
     Case(dtype, Hq, 1, 512, 48, lens, latent=True, seed=Hq + 1).check(lsa)
 
 
+@pytest.mark.parametrize("page", [1, 8, 16, 24, 32, 40, 64, 96, 128])
+@pytest.mark.parametrize("window,layout", [(0, "nshd"), (0, "nhsd"), (203, "nshd"), (256, "nhsd")])
+def test_attention_latent_pages_and_windows(lsa, page, window, layout):
+    """Rows that lie side by side in a page or do not, windows that begin inside a tile, bad pages, two latent heads."""
+    c = Case("bf16", 40, 2, 512, page, [1, 64, 200, 0, 1000, 3001, 128], latent=True, seed=page, window=window, layout=layout)
+    c.check(lsa)
+    table = c.table.copy()
+    table[4, 300 // page], table[5, 2900 // page], table[2, 0] = -1, 1 << 29, -7
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    c.check(lsa, table=table, err=err)
+    assert err.item() == (1 if window == 0 or 2900 >= 3001 - window else 0)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_attention_split_over_the_length(lsa, dtype):
     Case(dtype, 8, 1, 128, 64, [20001], seed=1).check(lsa)
