@@ -389,7 +389,8 @@ typedef struct lsa_page_cache {
  * Q         [B, Hq, D]: F32 with an F32 cache, BF16 with a BF16 or E4M3 one;
  *           sequence b starts at element b * q_stride.
  * out       [B, Hq, D] of Q's type, contiguous.   lse  [B, Hq] fp32 or NULL.
- * table     device int32, row b of max_pages page indices at b * table_stride.
+ * table     device int32, row b of max_pages page indices at b * table_stride;
+ *           max_pages * page_size at most 2^30.
  * seq_len   device int32 [B].  Below 0 counts as 0; above max_pages * page_size
  *           it is cut there and *err = LSA_ERR_CAPACITY.
  * A page index outside [0, n_pages) leaves its entries out and *err =
@@ -398,10 +399,13 @@ typedef struct lsa_page_cache {
  *           aligned; contents need not be initialised; calls that share it must
  *           not overlap.  The size is that of the current device.
  * err       device error word or NULL.
- * Products and sums are held in fp32 (E4M3 rows enter exactly); each query's
- * entries are split over the device's SMs and joined in a fixed order, so the
- * same call gives the same bits.  One launch where a sequence's table holds few
- * entries, else two.
+ *           A wait inside a kernel that ran out (2 s) shows as LSA_ERR_TIMEOUT there;
+ *           the call's outputs are then not to be used.
+ * Products and sums are held in fp32 (E4M3 rows enter exactly, but for value rows
+ * whose scale is below 2^-100, which lose low bits); each query's entries are
+ * split over the device's SMs and joined in a fixed order, so the same call gives
+ * the same bits.  One launch where a sequence's table holds few entries, else
+ * two.
  * ---------------------------------------------------------------------- */
 size_t lsa_paged_attn_workspace_size(const lsa_page_cache *cache, int32_t B, int32_t Hq);
 lsa_status lsa_paged_attn(const void *Q, lsa_dtype q_dtype, int64_t q_stride, const lsa_page_cache *cache,
@@ -428,8 +432,9 @@ lsa_status lsa_paged_attn(const void *Q, lsa_dtype q_dtype, int64_t q_stride, co
  * q, k, v   [T, Hq, D], [T, Hkv, D], [T, Hkv, D] of `dtype` (F32 or BF16); token t
  *           starts at element t * q_stride (k_stride, v_stride), so that they may
  *           be parts of one projection's output.  k NULL: queries only.
- * q_out, k_out  likewise; may be q and k themselves (same strides).  k_out may be
- *           NULL where a cache takes the keys.
+ * q_out, k_out  likewise; may be q and k themselves (same strides), and overlap
+ *           nothing else of the call (refused).  k_out may be NULL where a cache
+ *           takes the keys.
  * q_weight, k_weight  [D] of `dtype`, or NULL (no norm of those heads).
  * pos       device int32 [T], required with rot_dim > 0.
  * rope      NULL: no rotation.  rope->freq: device fp64 [rot_dim / 2], radians per
@@ -489,10 +494,11 @@ lsa_status lsa_rope_frequencies(lsa_rope_kind kind, int32_t rot_dim, double base
  * free ones of the lowest index, in the order of the call's rows: the same books
  * give the same pages.
  *
- * lsa_page_grow and lsa_page_fork either do all of a call or nothing: where the pool has too few free pages or a row would pass max_pages,
- * *err = LSA_ERR_CAPACITY; where a row index is out of range (or, for a fork, a
- * dst row is not empty, is named twice or is a src too), *err = LSA_ERR_INVALID; and the books
- * stay as they are (and a fork's list of copies is empty).  Page indices
+ * lsa_page_grow and lsa_page_fork either do all of a call or nothing: where the
+ * pool has too few free pages or a row would pass max_pages, *err =
+ * LSA_ERR_CAPACITY; where a row index is out of range (or, for a fork, a dst row
+ * is not empty, is named twice or is a src too), *err = LSA_ERR_INVALID; and the
+ * books stay as they are (and a fork's list of copies is empty).  Page indices
  * outside [0, n_pages) in the books are never followed.
  * Limits: n_rows <= 65536, n_pages <= 2^24, max_pages * page_size < 2^31.  `err` may
  * be NULL.

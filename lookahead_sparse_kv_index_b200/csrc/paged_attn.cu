@@ -186,8 +186,9 @@ extern "C" lsa_status lsa_paged_attn(const void *Q, lsa_dtype q_dtype, int64_t q
     LSA_CHECK_ARG(aligned16(Q) && aligned16(out), "lsa_paged_attn: Q and out must be 16-byte aligned");
     LSA_CHECK_ARG(max_pages >= 1 && table_stride >= max_pages && table_stride < (int64_t(1) << 40),
                   "lsa_paged_attn: max_pages=%d table_stride=%lld", max_pages, (long long)table_stride);
-    LSA_CHECK_ARG(int64_t(max_pages) * cache->page_size < (int64_t(1) << 31),
-                  "lsa_paged_attn: a table row reaches 2^31 entries or more");
+    // (places of entries are int32 in the kernels, which step past a sequence's end by up to a tile of every warp)
+    LSA_CHECK_ARG(int64_t(max_pages) * cache->page_size <= (int64_t(1) << 30),
+                  "lsa_paged_attn: a table row reaches more than 2^30 entries");
     LSA_CHECK_ARG(window >= 0, "lsa_paged_attn: window=%d", window);
     LSA_CHECK_ARG(scale > 0.0f && scale < 1e30f, "lsa_paged_attn: scale must be positive and finite");
     const AttnPlan p = plan_of(*cache, Hq);
@@ -220,7 +221,7 @@ extern "C" lsa_status lsa_paged_attn(const void *Q, lsa_dtype q_dtype, int64_t q
     a.q_f32 = q_dtype == LSA_F32;
     const int64_t most = window > 0 && window < a.reach ? window : a.reach;
     const int64_t segments = int64_t(B) * cache->Hkv * p.HG;
-    a.whole = most <= int64_t(kWholeUnits) * p.tile && segments < (int64_t(1) << 31);
+    a.whole = most <= int64_t(kWholeUnits) * p.tile && segments < (int64_t(1) << 30);
     const int grid = a.whole ? int(segments) : p.grid;
     a.by_segment = segments <= grid;
     const int heads = cache->Hkv * p.HG;

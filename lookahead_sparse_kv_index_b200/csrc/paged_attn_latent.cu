@@ -577,7 +577,7 @@ paged_attn_latent(const __grid_constant__ CUtensorMap rows_map, AttnArgs a, int 
     __syncwarp();
     __syncthreads();
     if (*abort_v) {
-        // scores that were sent and not waited for land well within this time
+        // scores and rows that are on their way and were not waited for land well within this time
         const uint64_t t0 = global_timer_ns();
         while (global_timer_ns() - t0 < 1000000) {}
         __syncwarp();

@@ -42,7 +42,6 @@ struct QkArgs {
     const double *freq;
     CacheView cache;
     int32_t append;              // 0: no cache, 1: rows of the inputs' type, 2: e4m3 rows
-    int32_t latent;
     const int32_t *table, *seq, *at;
     int64_t table_stride;
     int32_t n_rows;
@@ -452,6 +451,17 @@ lsa_status launch_vp(const QkArgs &a, unsigned grid, cudaStream_t st) {
     return launch_as<T, VP, 1, 0>(a, grid, st);
 }
 
+// Whether two arrays of T rows share bytes (rows `as` and `bs` bytes apart, `aw` and `bw` wide).  Of arrays with different
+// strides, whose rows might still pass each other, it is enough that the ranges meet.
+bool overlap(const void *a, int64_t as, int64_t aw, const void *b, int64_t bs, int64_t bw, int64_t T) {
+    if (!a || !b) return false;
+    const int64_t x = int64_t(reinterpret_cast<uintptr_t>(a)), y = int64_t(reinterpret_cast<uintptr_t>(b));
+    if (x + (T - 1) * as + aw <= y || y + (T - 1) * bs + bw <= x) return false;
+    if (as != bs) return true;
+    const int64_t d = ((y - x) % as + as) % as;      // of a's row to the next of b's
+    return d < aw || d + bw > as;
+}
+
 }  // namespace
 }  // namespace lsa
 
@@ -490,8 +500,15 @@ extern "C" lsa_status lsa_qk_norm_rope(const void *q, int64_t q_stride, void *q_
     LSA_CHECK_ARG(k || (!k_out && !v && !cache && !k_weight),
                   "lsa_qk_norm_rope: k_out, v, k_weight and a cache go with k");
     LSA_CHECK_ARG(!k || k_out || cache, "lsa_qk_norm_rope: k needs k_out or a cache");
-    LSA_CHECK_ARG((q_out != q || q_out_stride == q_stride) && (!k_out || k_out != k || k_out_stride == k_stride),
-                  "lsa_qk_norm_rope: an output in place of its input has the same stride");
+    // an output may be its own input, each of whose rows is read by the warp that writes it; any other overlap is a race
+    for (int o = 1; o < 5; o += 2)
+        for (int x = 0; x < 5; ++x) {
+            const bool own = x == o - 1 && in[x].p == in[o].p && in[x].stride == in[o].stride;
+            LSA_CHECK_ARG(x == o || own || !overlap(in[o].p, in[o].stride * e, in[o].heads * D * e, in[x].p,
+                                                    in[x].stride * e, in[x].heads * D * e, T),
+                          "lsa_qk_norm_rope: %s overlaps %s (an output in place of its input has the same strides)",
+                          in[o].name, in[x].name);
+        }
     LSA_CHECK_ARG((!q_weight || aligned16(q_weight)) && (!k_weight || aligned16(k_weight)),
                   "lsa_qk_norm_rope: weights must be 16-byte aligned");
     LSA_CHECK_ARG(eps >= 0.f && eps < 1e30f, "lsa_qk_norm_rope: eps must be finite and not negative");
@@ -508,8 +525,7 @@ extern "C" lsa_status lsa_qk_norm_rope(const void *q, int64_t q_stride, void *q_
                             "lsa_qk_norm_rope: the cache's rows are of dtype, or E4M3");
         LSA_CHECK_ARG(cache->Hkv == Hkv && cache->D == D, "lsa_qk_norm_rope: the cache has Hkv=%d D=%d, not %d and %d",
                       cache->Hkv, cache->D, Hkv, D);
-        a.latent = cache->v == cache->k;
-        LSA_CHECK_ARG(a.latent == (v == nullptr), "lsa_qk_norm_rope: v is required, unless the cache is latent");
+        LSA_CHECK_ARG((cache->v == cache->k) == (v == nullptr), "lsa_qk_norm_rope: v is required, unless the cache is latent");
         LSA_CHECK_ARG(table && at, "lsa_qk_norm_rope: a cache needs table and at");
         LSA_CHECK_ARG(n_rows >= 1 && max_pages >= 1 && table_stride >= max_pages && table_stride < (int64_t(1) << 40) &&
                           int64_t(max_pages) * cache->page_size < (int64_t(1) << 31),

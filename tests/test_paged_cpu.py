@@ -68,6 +68,14 @@ def test_attention_rejects_bad_arguments(lsa, kw, status):
     assert lsa.lib.lsa_last_error() != b""
 
 
+def test_attention_rejects_reaches_past_int32_steps(lsa):
+    """Places of entries are int32 and step past the end: 2^30 entries a row are the limit."""
+    size = _cache(lsa).page_size
+    most = (1 << 30) // size
+    assert _attn(lsa, mp=most + 1, ts=most + 1) == 1 and b"2^30" in lsa.lib.lsa_last_error()
+    assert _attn(lsa, mp=most, ts=most, scale=0.0) == 1 and b"scale" in lsa.lib.lsa_last_error()
+
+
 def test_attention_workspace_does_not_depend_on_lengths(lsa):
     c = _cache(lsa)
     size = lsa.lib.lsa_paged_attn_workspace_size(ctypes.byref(c), 1, 4)
@@ -102,6 +110,21 @@ def _qk(lsa, cache=None, rope=None, **kw):
 def test_norm_rope_rejects_bad_arguments(lsa, kw, status):
     assert _qk(lsa, **kw) == status
     assert lsa.lib.lsa_last_error() != b""
+
+
+def test_norm_rope_rejects_outputs_over_other_inputs(lsa):
+    """An output may be its own input; over any other operand, rows would be written before they are read."""
+    c, row = _cache(lsa), 2 * 64 * 2                                       # bytes of a token's keys
+    for kw in (dict(qo=3 * BIG), dict(ko=BIG), dict(qo=4 * BIG), dict(ko=5 * BIG),      # k, q, k_out, v
+               dict(qo=BIG + 16), dict(ko=3 * BIG + row), dict(ko=3 * BIG - row + 16),  # a shifted input of its own
+               dict(k=4 * BIG, v=4 * BIG), dict(q=2 * BIG + 4 * 64 * 2)):
+        assert _qk(lsa, cache=c, **kw) == 1, kw
+        assert b"overlaps" in lsa.lib.lsa_last_error(), kw
+    # parts of one projection's rows [q | k | v], in place, pass this check (and fail the next)
+    one = dict(q=BIG, qo=BIG, k=BIG + 4 * 64 * 2, ko=BIG + 4 * 64 * 2, v=BIG + 6 * 64 * 2, qs=512, qos=512, ks=512,
+               kos=512, vs=512)
+    assert _qk(lsa, cache=c, **one, eps=-1.0) == 1 and b"eps" in lsa.lib.lsa_last_error()
+    assert _qk(lsa, cache=c, **{**one, "ko": BIG + 5 * 64 * 2}) == 1 and b"overlaps" in lsa.lib.lsa_last_error()
 
 
 def test_norm_rope_rejects_bad_rotations_and_caches(lsa):
