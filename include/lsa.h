@@ -530,7 +530,7 @@ lsa_status lsa_page_free(const lsa_page_table *pt, const int32_t *rows, int32_t 
  * (both may be the books' own, to pack in place), the moves to move_src / move_dst [n_pages] (-1 padded) and their
  * number to n_moves [1], for lsa_page_copy on each layer's cache.  Afterwards pages L .. n_pages - 1 are free.
  * workspace: lsa_page_compact_workspace_size(n_pages) bytes, 16-byte aligned.  Two launches, or
- * three for a pool of more than 65536 pages. */
+ * three for a pool of more than 16384 pages. */
 size_t lsa_page_compact_workspace_size(int64_t n_pages);
 lsa_status lsa_page_compact(const lsa_page_table *pt, int32_t *table_out, int32_t *refs_out, int32_t *move_src,
                             int32_t *move_dst, int32_t *n_moves, void *workspace, size_t ws_bytes, void *stream);

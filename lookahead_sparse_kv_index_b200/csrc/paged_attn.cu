@@ -12,7 +12,8 @@ namespace {
 
 // Joins a segment's partials (paged_attn.cuh): CTA (r, i) those of record r, for head i of the group.  A group of
 // D / 4 threads adds 16-byte pieces of every kGroups-th partial; its first loads are on their way while the weights are
-// made.
+// made.  Its bytes are few (two partials a CTA of the kernel before); what it costs is a launch and three dependent trips
+// to memory, about 3 us of a call.
 constexpr int kCombineThreads = 256, kAhead = 4;
 __global__ void __launch_bounds__(kCombineThreads) paged_attn_combine(AttnArgs a) {
     __shared__ float red[2][kCombineThreads / 32];
@@ -94,8 +95,10 @@ AttnPlan plan_of(const lsa_page_cache &c, int Hq) {
     return latent_supported(c, Hq) ? plan_latent(c, Hq) : plan_mma(c, Hq);
 }
 
-// A segment of so few units is done by one CTA, without partials and a second launch.
-constexpr int kWholeUnits = 8;
+// Where no segment has more tiles than this, each is done by one CTA, without partials and a second launch (bf16, 8 kv
+// heads of 128, tiles of 64 entries, against the split: one sequence of 4 tiles 6.4 us against 8.9, of 8 tiles 9.9 against
+// 9.0, of 16 tiles 16.8 against 9.1; 75 sequences of up to 8 tiles 15.5 against 20.2, of up to 16 tiles 25.8 against 24.6).
+constexpr int kWholeTiles = 8;
 
 }  // namespace
 
@@ -221,7 +224,7 @@ extern "C" lsa_status lsa_paged_attn(const void *Q, lsa_dtype q_dtype, int64_t q
     a.q_f32 = q_dtype == LSA_F32;
     const int64_t most = window > 0 && window < a.reach ? window : a.reach;
     const int64_t segments = int64_t(B) * cache->Hkv * p.HG;
-    a.whole = most <= int64_t(kWholeUnits) * p.tile && segments < (int64_t(1) << 30);
+    a.whole = most <= int64_t(kWholeTiles) * p.tile && segments < (int64_t(1) << 30);
     const int grid = a.whole ? int(segments) : p.grid;
     a.by_segment = segments <= grid;
     const int heads = cache->Hkv * p.HG;

