@@ -3,9 +3,10 @@
 // The books are whole numbers, so every result is exact and the same from run to run: new pages are the free ones of
 // the lowest index, handed out in the order of the call's rows, and the counts change by integer atomics.  Growing and
 // forking are one CTA: it adds up what the call needs, counts free pages from index 0 until they suffice (nothing is
-// written before that), and goes over them again handing each to its row; 1024 threads take 16 counts each a round, so
-// a pool of 64K pages is four rounds a pass, and a round costs about a microsecond of latency.  The copy of whole pages
-// is bound by HBM: 202 MB copied to other pages take 62 us, the copy rate.
+// written before that), and lists them, round by round, for a thread each to hand to its row; 1024 threads take 16
+// counts each a round, so a pool of 64K pages is four rounds a pass.  Their latency is what they cost: a free, a fork of
+// 20 rows and its copies take 11 us.  The copy of whole pages is bound by HBM: 202 MB copied to other pages take 62 us,
+// the copy rate.
 #include "paged.cuh"
 
 namespace lsa {
@@ -54,52 +55,78 @@ __device__ __forceinline__ V block_scan(V v, V *part, V *total) {
     return before + s;
 }
 
-// The free pages among the 16 of this thread in round `r`, as a mask.
-__device__ __forceinline__ uint32_t free_mask(const Books &bk, int64_t r) {
-    const int64_t p0 = r * kRound + int64_t(threadIdx.x) * kPer;
-    uint32_t m = 0;
-    if (p0 + kPer <= bk.n_pages && (reinterpret_cast<uintptr_t>(bk.refs) & 15) == 0) {
-        int4 v[kPer / 4];
+// The counts of the 16 pages of this thread in round `r`, and which of them are free (0), as a mask.
+struct Counts {
+    int4 v[kPer / 4];
+    __device__ __forceinline__ void load(const Books &bk, int64_t r) {
+        const int64_t p0 = r * kRound + int64_t(threadIdx.x) * kPer;
+        if (p0 + kPer <= bk.n_pages && (reinterpret_cast<uintptr_t>(bk.refs) & 15) == 0) {
 #pragma unroll
-        for (int i = 0; i < kPer / 4; ++i) v[i] = reinterpret_cast<const int4 *>(bk.refs + p0)[i];
+            for (int i = 0; i < kPer / 4; ++i) v[i] = reinterpret_cast<const int4 *>(bk.refs + p0)[i];
+        } else {
+            auto one = [&](int i) { return p0 + i < bk.n_pages ? bk.refs[p0 + i] : 1; };
+#pragma unroll
+            for (int i = 0; i < kPer / 4; ++i) v[i] = make_int4(one(4 * i), one(4 * i + 1), one(4 * i + 2), one(4 * i + 3));
+        }
+    }
+    __device__ __forceinline__ uint32_t free() const {
+        uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < kPer / 4; ++i)
             m |= (uint32_t(v[i].x == 0) | uint32_t(v[i].y == 0) << 1 | uint32_t(v[i].z == 0) << 2 |
                   uint32_t(v[i].w == 0) << 3)
                  << (4 * i);
-    } else {
-        for (int i = 0; i < kPer; ++i)
-            if (p0 + i < bk.n_pages && bk.refs[p0 + i] == 0) m |= 1u << i;
+        return m;
     }
-    return m;
+};
+
+// The pool's free pages, round by round (whole block).  Round 0's counts are asked for before anything else and their sum
+// is kept: most calls end there.
+struct Free {
+    Counts counts0;
+    int upto0, total0;      // free pages of round 0 up to and with this thread's, all of its
+};
+__device__ __forceinline__ int free_of(const Books &bk, const Free &f, int64_t r, uint32_t *mask, int *total, int *part) {
+    if (r == 0) {
+        *mask = f.counts0.free();
+        *total = f.total0;
+        return f.upto0;
+    }
+    Counts c;
+    c.load(bk, r);
+    *mask = c.free();
+    return block_scan(__popc(*mask), part, total);
 }
 
-// Whether the pool has `need` free pages (whole block).  `mask0`: round 0's free pages, which its caller asks for before
-// anything else; most calls end there.
-__device__ bool enough_free(const Books &bk, int64_t need, uint32_t mask0, int *part) {
-    int64_t have = 0;
-    for (int64_t r = 0; have < need && r * kRound < bk.n_pages; ++r) {
+// Whether the pool has `need` free pages.
+__device__ bool enough_free(const Books &bk, int64_t need, Free &f, int *part) {
+    f.upto0 = block_scan(__popc(f.counts0.free()), part, &f.total0);
+    int64_t have = f.total0;
+    for (int64_t r = 1; have < need && r * kRound < bk.n_pages; ++r) {
+        uint32_t m;
         int total;
-        block_scan(__popc(r ? free_mask(bk, r) : mask0), part, &total);
+        free_of(bk, f, r, &m, &total, part);
         have += total;
     }
     return have >= need;
 }
 
-// Hands the `need` lowest free pages out (whole block): give(k, page) for the k-th, by one thread.  give may write the
-// page's own count.
+// Hands the `need` lowest free pages out: give(k, page) for the k-th, by one thread.  A round's pages are listed first, so
+// that neighbouring ones go to different threads (each handing out the free ones of its own sixteen, a call of 20 pages
+// took 10 us more).  give may write the page's own count.  `list`: kRound places of shared memory.
 template <typename F>
-__device__ void hand_out(const Books &bk, int64_t need, uint32_t mask0, int *part, F give) {
+__device__ void hand_out(const Books &bk, int64_t need, const Free &f, int *part, uint16_t *list, F give) {
     int64_t given = 0;
     for (int64_t r = 0; given < need && r * kRound < bk.n_pages; ++r) {
-        uint32_t m = r ? free_mask(bk, r) : mask0;
+        uint32_t m;
         int total;
-        int64_t k = given + block_scan(__popc(m), part, &total) - __popc(m);
-        for (; m && k < need; ++k) {
-            const int i = __ffs(m) - 1;
-            m &= m - 1;
-            give(k, int32_t(r * kRound + int64_t(threadIdx.x) * kPer + i));
-        }
+        int at = free_of(bk, f, r, &m, &total, part) - __popc(m);
+        for (; m; m &= m - 1) list[at++] = uint16_t(threadIdx.x * kPer + __ffs(m) - 1);
+        __syncthreads();
+        const int64_t left = need - given;
+        const int take = left < total ? int(left) : total;
+        for (int k = threadIdx.x; k < take; k += kBooks) give(given + k, int32_t(r * kRound + list[k]));
+        __syncthreads();
         given += total;
     }
 }
@@ -113,17 +140,18 @@ __device__ __forceinline__ uint32_t pages_of(const Books &bk, uint32_t n) {
     return (n + uint32_t(bk.page_size) - 1) / uint32_t(bk.page_size);
 }
 
-// What the threads' items need, summed up to each thread: first[t] in shared memory, the sum is returned.
-__device__ __forceinline__ int64_t prefix(int64_t mine, int64_t *first, int64_t *part) {
+// What the threads' items need, summed up to each thread: first[t] in shared memory, the sum is returned.  (A sum that
+// 32 bits do not hold is more than any pool has, and first is not used.)
+__device__ __forceinline__ int64_t prefix(int64_t mine, int32_t *first, int64_t *part) {
     int64_t total;
-    first[threadIdx.x + 1] = block_scan(mine, part, &total);
+    first[threadIdx.x + 1] = int32_t(block_scan(mine, part, &total));
     if (threadIdx.x == 0) first[0] = 0;
     __syncthreads();
     return total;
 }
 
 // The thread whose items hold the k-th page: first[t] <= k < first[t + 1].
-__device__ __forceinline__ int thread_of(const int64_t *first, int64_t k) {
+__device__ __forceinline__ int thread_of(const int32_t *first, int64_t k) {
     int lo = 0, hi = kBooks - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -133,11 +161,14 @@ __device__ __forceinline__ int thread_of(const int64_t *first, int64_t k) {
 }
 
 __global__ void __launch_bounds__(kBooks) page_grow(Books bk, const int32_t *__restrict__ add, int32_t *err) {
-    __shared__ int64_t first[kBooks + 1], part64[33];
+    __shared__ int64_t part64[33];
+    __shared__ int32_t first[kBooks + 1];
     __shared__ int part[33];
+    __shared__ uint16_t list[kRound];
     pdl_launch_dependents();
     pdl_wait();
-    const uint32_t mask0 = free_mask(bk, 0);
+    Free free;
+    free.counts0.load(bk, 0);
     const int per = (bk.n_rows + kBooks - 1) / kBooks;
     const int r0 = min(bk.n_rows, int(threadIdx.x) * per), r1 = min(bk.n_rows, r0 + per);
     const int64_t reach = int64_t(bk.max_pages) * bk.page_size;
@@ -154,11 +185,11 @@ __global__ void __launch_bounds__(kBooks) page_grow(Books bk, const int32_t *__r
     for (int r = r0; r < r1; ++r) need += need_of(r, &have, &past);
     past = __syncthreads_or(past);
     const int64_t total = prefix(need, first, part64);
-    if (past || !enough_free(bk, total, mask0, part)) {
+    if (past || !enough_free(bk, total, free, part)) {
         if (threadIdx.x == 0) raise_err(err, LSA_ERR_CAPACITY);
         return;
     }
-    hand_out(bk, total, mask0, part, [&](int64_t k, int32_t page) {
+    hand_out(bk, total, free, part, list, [&](int64_t k, int32_t page) {
         const int t = thread_of(first, k);
         int64_t at = first[t];
         uint32_t have;
@@ -183,12 +214,15 @@ __global__ void __launch_bounds__(kBooks) page_grow(Books bk, const int32_t *__r
 __global__ void __launch_bounds__(kBooks) page_fork_take(Books bk, const int32_t *__restrict__ src,
                                                          const int32_t *__restrict__ dst, int n, int32_t *copy_src,
                                                          int32_t *copy_dst, int32_t *err) {
-    __shared__ int64_t first[kBooks + 1], part64[33];
+    __shared__ int64_t part64[33];
+    __shared__ int32_t first[kBooks + 1];
     __shared__ int part[33];
+    __shared__ uint16_t list[kRound];
     __shared__ uint32_t named[kMaxRows / 32];
     pdl_launch_dependents();
     pdl_wait();
-    const uint32_t mask0 = free_mask(bk, 0);
+    Free free;
+    free.counts0.load(bk, 0);
     const int per = (n + kBooks - 1) / kBooks;
     const int i0 = min(n, int(threadIdx.x) * per), i1 = min(n, i0 + per);
     auto part_filled = [&](int i) { return held_entries(bk, src[i]) % uint32_t(bk.page_size) > 0; };
@@ -211,7 +245,7 @@ __global__ void __launch_bounds__(kBooks) page_fork_take(Books bk, const int32_t
         for (int i = i0; i < i1; ++i) bad |= (named[src[i] >> 5] >> (src[i] & 31)) & 1u;
     bad = __syncthreads_or(bad);
     const int64_t total = prefix(need, first, part64);
-    if (bad || !enough_free(bk, total, mask0, part)) {
+    if (bad || !enough_free(bk, total, free, part)) {
         if (threadIdx.x == 0) raise_err(err, bad ? LSA_ERR_INVALID : LSA_ERR_CAPACITY);
         for (int i = threadIdx.x; i < n; i += kBooks) {
             copy_src[i] = -2;
@@ -222,7 +256,7 @@ __global__ void __launch_bounds__(kBooks) page_fork_take(Books bk, const int32_t
     for (int i = i0; i < i1; ++i) {
         if (!part_filled(i)) copy_src[i] = copy_dst[i] = -1;
     }
-    hand_out(bk, total, mask0, part, [&](int64_t k, int32_t page) {
+    hand_out(bk, total, free, part, list, [&](int64_t k, int32_t page) {
         const int t = thread_of(first, k);
         int64_t at = first[t];
         for (int i = t * per;; ++i) {
