@@ -47,6 +47,7 @@ struct QkArgs {
     int32_t n_rows;
     int64_t reach;
     int32_t *err;
+    int32_t mixed;               // 1: parts hold whole pairs, some of which may turn
     int32_t lpr;                 // lanes of a row, a power of two
     int32_t nq, nk, nv;          // rounds of a token's queries, keys, values: 32 / lpr rows each
     int64_t share, spare;        // rounds of a warp; the first `spare` warps have one more
@@ -133,8 +134,8 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&x)[N], floa
 }
 
 // T: element type of q, k, v; VP: pairs of a unit; MU: units of a lane; LPR: lanes of a row (0: a.lpr); IL: interleaved
-// pairs.
-template <typename T, int VP, int MU, int LPR, bool IL>
+// pairs; MIX: a part of a unit may hold pairs that turn and pairs that do not (whole pairs alone).
+template <typename T, int VP, int MU, int LPR, bool IL, bool MIX>
 __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(QkArgs a) {
     constexpr int E = int(sizeof(T));
     constexpr int kPart = VP * E, kSlot = 32 * 2 * MU * kPart;
@@ -151,8 +152,9 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(QkArgs a) {
     // A unit's two parts of VP elements: byte offsets, and its first pair (of each part, where the parts hold whole pairs;
     // `turns`: whether they turn).  Lanes are neighbours in both parts, so that their accesses fill whole sectors.
     constexpr bool kWhole = IL && VP > 1;
+    static_assert(kWhole || !MIX, "parts of halves of pairs turn as one");
     int ia[MU], ib[MU], pa[MU], pb[MU];
-    bool mine[MU], turns[MU][2];
+    bool mine[MU], turns[MU][MIX ? VP : 2];
 #pragma unroll
     for (int m = 0; m < MU; ++m) {
         const int u = lane + lpr * m, p = u * VP;
@@ -167,8 +169,13 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(QkArgs a) {
             ib[m] = (IL ? 2 * p + 1 : p < half ? p + half : a.rot + rest + (p - half)) * E;
             pa[m] = pb[m] = p;
         }
-        turns[m][0] = pa[m] < half;
-        turns[m][1] = pb[m] < half;
+        if constexpr (MIX) {
+#pragma unroll
+            for (int e = 0; e < VP; ++e) turns[m][e] = (e < VP / 2 ? pa[m] + e : pb[m] + e - VP / 2) < half;
+        } else {
+            turns[m][0] = pa[m] < half;
+            turns[m][1] = pb[m] < half;
+        }
     }
     pdl_launch_dependents();
     pdl_wait();
@@ -301,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(QkArgs a) {
 #pragma unroll
                     for (int e = 0; e < VP; ++e) {
                         const int second = kWhole && e >= VP / 2;
-                        const float2 c = turns[m][second] ? cs[second ? pb[m] + e - VP / 2 : pa[m] + e] : make_float2(1.f, 0.f);
+                        const float2 c = turns[m][MIX ? e : second] ? cs[second ? pb[m] + e - VP / 2 : pa[m] + e] : make_float2(1.f, 0.f);
                         const float u = IL ? wt[2 * e] : wt[e], v = IL ? wt[2 * e + 1] : wt[VP + e];
                         ac[m][e] = u * c.x;
                         as[m][e] = u * c.y;
@@ -349,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(QkArgs a) {
                         for (int e = 0; e < VP; ++e) {
                             float &x0 = x[m][IL ? 2 * e : e], &x1 = x[m][IL ? 2 * e + 1 : VP + e];
                             float p = x0 * ac[m][e], q = x1 * bc[m][e];
-                            if (turns[m][kWhole && e >= VP / 2]) {       // (an element that does not turn never meets its partner)
+                            if (turns[m][MIX ? e : kWhole && e >= VP / 2]) {       // (an element that does not turn never meets its partner)
                                 p = fmaf(-x1, bs[m][e], p);
                                 q = fmaf(x0, as[m][e], q);
                             }
@@ -423,10 +430,10 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(QkArgs a) {
     }
 }
 
-template <typename T, int VP, int MU, int LPR>
+template <typename T, int VP, int MU, int LPR, bool MIX = false>
 lsa_status launch_as(const QkArgs &a, unsigned grid, cudaStream_t st) {
     const size_t smem = size_t(kWarps) * (size_t(kAhead) * 32 * 2 * MU * VP * sizeof(T) + size_t(a.rot / 2) * 8);
-    auto *kernel = a.interleaved ? qk_norm_rope<T, VP, MU, LPR, true> : qk_norm_rope<T, VP, MU, LPR, false>;
+    auto *kernel = a.interleaved ? qk_norm_rope<T, VP, MU, LPR, true, MIX> : qk_norm_rope<T, VP, MU, LPR, MIX, MIX>;
     LSA_CUDA(ensure_smem(kernel, smem));
     LSA_CUDA(launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, st, a));
     LSA_LAUNCHED("qk_norm_rope");
@@ -438,6 +445,10 @@ lsa_status launch_vp(const QkArgs &a, unsigned grid, cudaStream_t st) {
     const int units = (a.D / 2 / VP + a.lpr - 1) / a.lpr;    // of a lane: at most 8 / VP
     if constexpr (VP * sizeof(T) == 16) {
         constexpr int kRow = 128 / 2 / VP;
+        if (a.mixed) {
+            if (units == 1) return launch_as<T, VP, 1, 0, true>(a, grid, st);
+            return launch_as<T, VP, 2, 0, true>(a, grid, st);
+        }
         if (a.lpr == kRow / 2) return launch_as<T, VP, 1, kRow / 2>(a, grid, st);
         if (a.lpr == kRow) return launch_as<T, VP, 1, kRow>(a, grid, st);
         if (a.lpr == 2 * kRow && units == 1) return launch_as<T, VP, 1, 2 * kRow>(a, grid, st);
@@ -569,10 +580,13 @@ extern "C" lsa_status lsa_qk_norm_rope(const void *q, int64_t q_stride, void *q_
     a.n_rows = n_rows;
     a.err = err;
     a.row_bytes = int32_t(D * e);
-    // the widest unit that the sizes allow, of parts whose pairs all turn or all stay
+    // The widest unit that the sizes allow, of parts whose pairs all turn or all stay.  Where pairs are interleaved the
+    // widest always does, with a flag for each pair (8319 tokens of 24 bf16 heads of 256 with 38 turning: 39 us, and 103 with
+    // units of one pair): a kernel of its own, since the flags cost a few instructions.
     int vp = dtype == LSA_BF16 ? 8 : 4;
     auto fits = [&](int n) { return rot / 2 % n == 0 && (D - rot) / 2 % n == 0; };
-    while (!fits(vp)) vp /= 2;
+    a.mixed = a.interleaved && !fits(vp);
+    while (!a.mixed && !fits(vp)) vp /= 2;
     a.lpr = 1;
     while (a.lpr < 32 && a.lpr * vp < D / 2) a.lpr *= 2;
     const int groups = 32 / a.lpr;

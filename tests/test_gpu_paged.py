@@ -383,6 +383,31 @@ def test_norm_rope_append(lsa, dtype, kind, T, Hq, Hkv, D, rot, interleaved, nor
         assert (c[left].float() == 3).all() and (s is None or (s[left] == 9).all()), name
 
 
+@pytest.mark.parametrize("dtype,kind", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "e4m3")])
+@pytest.mark.parametrize("shape", [(11, 3, 2, 256, 38), (300, 5, 1, 64, 20), (4, 2, 1, 512, 98), (2, 3, 3, 16, 10),
+                                   (3, 2, 1, 80, 78)])
+def test_norm_rope_interleaved_parts_that_turn_in_part(lsa, dtype, kind, shape):
+    """Interleaved pairs of which a lane's 16 bytes hold some that turn and some that do not."""
+    test_norm_rope_append(lsa, dtype, kind, *shape, True, True)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D,rot,interleaved", [(64, 20, True), (256, 38, True), (64, 20, False), (128, 64, True)])
+def test_elements_that_do_not_turn_never_meet_their_neighbours(lsa, dtype, D, rot, interleaved):
+    g = torch.Generator(device="cuda").manual_seed(D + rot)
+    x = torch.randn((5, 3, D), generator=g, device="cuda").to(DT[dtype])
+    bad = x.clone()
+    bad[:, :, rot], bad[:, :, rot + 1], bad[:, :, D - 1] = float("inf"), float("nan"), -float("inf")
+    freq, _ = lsa.rope_frequencies(rot)
+    rope, pos, out, want = lsa.Rope(freq.cuda(), interleaved), i32(range(5)), torch.empty_like(x), torch.empty_like(x)
+    lsa.qk_norm_rope(x, q_out=want, pos=pos, rope=rope)
+    lsa.qk_norm_rope(bad, q_out=out, pos=pos, rope=rope)
+    want[:, :, rot], want[:, :, rot + 1], want[:, :, D - 1] = float("inf"), float("nan"), -float("inf")
+    bits = {"f32": torch.int32, "bf16": torch.int16}[dtype]
+    keep = torch.arange(D, device="cuda") != rot + 1
+    assert torch.equal(out[:, :, keep].view(bits), want[:, :, keep].view(bits)) and out[:, :, rot + 1].isnan().all()
+
+
 def test_norm_rope_in_place_queries_only_and_latent_append(lsa):
     g = torch.Generator(device="cuda").manual_seed(2)
     x = torch.randn((9, 6, 64), generator=g, device="cuda")
