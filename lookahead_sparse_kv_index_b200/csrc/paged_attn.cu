@@ -96,7 +96,7 @@ AttnPlan plan_of(const lsa_page_cache &c, int Hq) {
 }
 
 // Where no segment has more than this many tiles, each is done by one CTA, without partials and a second launch: up to 5
-// tiles always, up to 8 where the segments are a quarter of the grid's CTAs or more.  Whole against split: bf16, 8 kv heads
+// tiles always, up to 8 where the segments are a sixth of the grid's CTAs or more.  Whole against split: bf16, 8 kv heads
 // of 128, one sequence of 5 tiles 7.1 us against 9.1, of 8 tiles 9.6 against 9.1, 16 sequences of 8 tiles 12.5 against 15.2;
 // latent, 128 heads, one sequence of 5 tiles 18.5 against 18.6, of 8 tiles 23.5 against 18.8, 32 of 8 tiles 24.9 against
 // 41.7; fp32, 8 kv heads, one of 4 tiles 9.1 against 10.1, of 8 tiles 15.0 against 10.2, 32 of 8 tiles 20.6 against 29.7.
@@ -227,7 +227,7 @@ extern "C" lsa_status lsa_paged_attn(const void *Q, lsa_dtype q_dtype, int64_t q
     a.q_f32 = q_dtype == LSA_F32;
     const int64_t most = window > 0 && window < a.reach ? window : a.reach;
     const int64_t segments = int64_t(B) * cache->Hkv * p.HG;
-    a.whole = most <= int64_t(segments * 4 >= p.grid ? kWholeMany : kWholeFew) * p.tile && segments < (int64_t(1) << 30);
+    a.whole = most <= int64_t(segments * 6 >= p.grid ? kWholeMany : kWholeFew) * p.tile && segments < (int64_t(1) << 30);
     const int grid = a.whole ? int(segments) : p.grid;
     a.by_segment = segments <= grid;
     const int heads = cache->Hkv * p.HG;
