@@ -2,16 +2,18 @@
 // paged_attn.cuh says how the work is cut).
 //
 // HBM bounds it as long as no row is read for more than one group of heads, so o of all of a group's NH query heads is
-// kept in registers: LT lanes share an entry, each with KC 16-byte pieces of its row, and NH * KC * 4 <= 64.  Eight heads
-// take twice the lanes an entry of four, which costs shuffles, not bytes (sixteen on 32 lanes were slower than two
-// groups of eight: 463 us against 2 x 186 for 537 MB of rows).  As in the tensor-core kernel every
-// warp is a pipeline of its own, here with stages of 8 KB of K and V rows (cp.async); a lane works on two entries of a
-// step at a time, and every group of LT lanes runs its own online softmax, with a reference that moves only when a score
-// passes it by 2^8.  The groups and warps meet at the end of a piece.
+// kept in registers: LT lanes share an entry, each with KC 16-byte pieces of its row, and NH * KC * 4 <= 64.  LT is the
+// least that this allows, since an entry's shuffles and exponentials are shared by its lanes (heads of 32 elements: 87 us
+// with 4 lanes an entry, 104 with 8; of 64 elements 70 and 75).  Eight heads take twice the lanes an entry of four, which
+// costs shuffles, not bytes (sixteen on 32 lanes were slower than two groups of eight: 463 us against 2 x 186 for 537 MB of
+// rows).  As in the tensor-core kernel every warp is a pipeline of its own, here with stages of 8 KB of K and V rows
+// (cp.async); a lane works on two entries of a step at a time, and every group of LT lanes runs its own online softmax,
+// with a reference that moves only when a score passes it by 2^8.  The groups and warps meet at the end of a piece.
 //
 // Measured: 537 MB of rows under 4 query heads a kv head 115 us (4.7 TB/s, 72% of the copy rate), under 8 heads 186 us:
-// four products an element and head, so the fp32 pipe and HBM are near each other at 4 heads.  A batch of 17 MB with a
-// window takes 13 us, of which 9 are the two launches' own latencies.
+// four products an element and head, so the fp32 pipe and HBM are near each other at 4 heads; 268 MB of heads of 64
+// elements 70 us (59%), of 32 elements 86 us (48%), by the work an entry costs whatever its length.  A batch of 17 MB with
+// a window takes 13 us, of which 9 are the two launches' own latencies.
 #include <limits.h>
 
 #include "paged_attn.cuh"
@@ -42,7 +44,9 @@ struct Shape {
     static constexpr int kStage = kMaxD <= 32 ? 32 : kMaxD <= 64 ? 16 : kMaxD <= 128 ? 8 : kMaxD <= 256 ? 4 : 2;
     static constexpr int kCopyLanes = kStage >= 4 ? 8 : 16;         // that copy a row
     static_assert(kStage % kStep == 0 && kStage * kCopyLanes % 32 == 0, "a stage is whole steps and whole copies");
-    static __host__ __device__ int stage(int D, bool latent) { return kStage * D * 4 * (latent ? 1 : 2) + 16; }
+    // bytes between staged rows: where two groups of lanes read neighbouring rows at once, an odd number of 64
+    static __host__ __device__ int pitch(int D) { return D * 4 + (LT == 4 && D % 32 == 0 ? 64 : 0); }
+    static __host__ __device__ int stage(int D, bool latent) { return kStage * pitch(D) * (latent ? 1 : 2) + 16; }
 };
 
 template <int LT, int KC, int NH>
@@ -53,7 +57,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_f32(AttnArgs a, int
     const int D = a.cache.D, nch = D / 4, row_bytes = D * 4;
     const bool latent = a.cache.v == a.cache.k;
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = lane / LT, dl = lane % LT;
-    const int stage_bytes = C::stage(D, latent), rows = C::kStage * row_bytes, v_at = latent ? 0 : rows;
+    const int pitch = C::pitch(D), stage_bytes = C::stage(D, latent), rows = C::kStage * pitch, v_at = latent ? 0 : rows;
     float *qs = reinterpret_cast<float *>(smem);                       // [NH][D]
     uint8_t *ring = smem + NH * row_bytes + size_t(warp) * stages * stage_bytes;
     // where the parts of a piece meet, over the stages
@@ -101,7 +105,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_f32(AttnArgs a, int
                     const int64_t o = __shfl_sync(0xffffffffu, off, r);
                     const bool ok = o >= 0;
                     const uint8_t *kf = ksrc + (ok ? o : 0), *vf = vsrc + (ok ? o : 0);
-                    const uint32_t to = smem_addr(st) + r * row_bytes;
+                    const uint32_t to = smem_addr(st) + r * pitch;
                     for (int i = cp; i < nch; i += C::kCopyLanes) {
                         cp_async16(to + i * 16, kf + i * 16, ok);
                         if (!latent) cp_async16(to + v_at + i * 16, vf + i * 16, ok);
@@ -160,8 +164,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_f32(AttnArgs a, int
                 for (int c = 0; c < KC; ++c) {
                     const int ch = c * LT + dl;
                     if (ch < nch) {
-                        const float4 x = *reinterpret_cast<const float4 *>(sk + t0 * row_bytes + ch * 16);
-                        const float4 y = *reinterpret_cast<const float4 *>(sk + t1 * row_bytes + ch * 16);
+                        const float4 x = *reinterpret_cast<const float4 *>(sk + t0 * pitch + ch * 16);
+                        const float4 y = *reinterpret_cast<const float4 *>(sk + t1 * pitch + ch * 16);
 #pragma unroll
                         for (int h = 0; h < NH; ++h) {
                             const float4 w = *reinterpret_cast<const float4 *>(qs + h * D + ch * 4);
@@ -207,8 +211,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_f32(AttnArgs a, int
                 for (int c = 0; c < KC; ++c) {
                     const int ch = c * LT + dl;
                     if (ch < nch) {
-                        const float4 x = *reinterpret_cast<const float4 *>(sv + t0 * row_bytes + ch * 16);
-                        const float4 y = *reinterpret_cast<const float4 *>(sv + t1 * row_bytes + ch * 16);
+                        const float4 x = *reinterpret_cast<const float4 *>(sv + t0 * pitch + ch * 16);
+                        const float4 y = *reinterpret_cast<const float4 *>(sv + t1 * pitch + ch * 16);
 #pragma unroll
                         for (int h = 0; h < NH; ++h) {
                             o[h][c][0] = fmaf(s0[h], x.x, fmaf(s1[h], y.x, o[h][c][0]));
@@ -288,8 +292,9 @@ struct Run {
 template <typename F>
 auto with_shape(int D, int G, F f) {
     const bool few = G <= 4;
-    if (D <= 32) return few ? f(Run<8, 1, 4>()) : f(Run<8, 1, 8>());
-    if (D <= 64) return few ? f(Run<8, 2, 4>()) : f(Run<8, 2, 8>());
+    if (D <= 16) return few ? f(Run<4, 1, 4>()) : f(Run<4, 1, 8>());
+    if (D <= 32) return few ? f(Run<4, 2, 4>()) : f(Run<4, 2, 8>());
+    if (D <= 64) return few ? f(Run<4, 4, 4>()) : f(Run<8, 2, 8>());
     if (D <= 96 && few) return f(Run<8, 3, 4>());
     if (D <= 128) return few ? f(Run<8, 4, 4>()) : f(Run<16, 2, 8>());
     if (D <= 192 && few) return f(Run<16, 3, 4>());
