@@ -281,6 +281,42 @@ def test_attention_same_bits_on_another_stream_in_a_graph_and_without_lse(lsa, d
     assert torch.equal(out, a) and torch.equal(lse, za)
 
 
+@pytest.mark.parametrize("Hq", [20, 128])
+def test_attention_latent_sharp_scores(lsa, Hq):
+    """Scores in the hundreds: the references move from tile to tile, and what was summed up is rescaled."""
+    Case("bf16", Hq, 1, 512, 64, [5, 300, 2000, 9000], latent=True, seed=Hq, q_scale=60.0).check(lsa)
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,D,tile,latent", [("bf16", 4, 1, 128, 64, False), ("e4m3", 4, 1, 128, 128, False),
+                                                       ("f32", 4, 1, 128, 32, False), ("bf16", 16, 1, 512, 64, True)])
+@pytest.mark.parametrize("B", [2, 30, 70])
+def test_attention_where_segments_are_whole_or_split(lsa, dtype, Hq, Hkv, D, tile, latent, B):
+    """Reaches of 5 and 8 tiles, where few and many segments change from one way to the other, and one entry more."""
+    for tiles in (5, 8):
+        for more in (0, 1):
+            n = tiles * tile + more
+            lens = [n, 0, n - 1, 1, tile] + [(37 * i) % (n + 1) for i in range(B)]
+            Case(dtype, Hq, Hkv, D, 1, lens[:B], latent=latent, seed=B + n).check(lsa)
+
+
+def test_attention_two_calls_at_once(lsa):
+    """Calls on two streams with workspaces of their own, over one cache."""
+    for dtype, Hq, D, latent in (("bf16", 8, 128, False), ("bf16", 40, 512, True), ("f32", 8, 64, False)):
+        c = Case(dtype, Hq, 1, D, 16, [3000, 1, 0, 9000, 700], latent=latent, seed=11)
+        want, lse = c.check(lsa)
+        cache, q, table, lens = c.cache(lsa), c.q.cuda(), i32(c.table), i32(c.lens)
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        ws = [torch.empty(lsa.paged_attn_workspace_size(cache, 5, Hq), dtype=torch.uint8, device="cuda") for _ in streams]
+        outs = [torch.zeros((6,) + want.shape, dtype=want.dtype, device="cuda") for _ in streams]
+        torch.cuda.synchronize()
+        for i in range(6):
+            for s, w, o in zip(streams, ws, outs):
+                lsa.paged_attn(q, cache, table, lens, o[i], w, scale=c.scale, stream=s)
+        torch.cuda.synchronize()
+        for o in outs:
+            assert all(torch.equal(x, want) for x in o)
+
+
 def test_attention_offsets_past_32_bits(lsa):
     """A cache of more than 2^32 bytes, with a sequence on its last pages."""
     n_pages, page, D = 70000, 64, 512                  # 4.6 GB of bf16 rows
@@ -710,3 +746,59 @@ def test_decode_steps_over_forked_and_packed_pages(lsa, kind):
     for _ in range(9):
         attend(append({1: 1, 3: 1, 4: 1, 5: 1}))
     assert err.item() == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_a_captured_decode_step_follows_the_books(lsa, kind):
+    """grow, norm/rotate/append and attention captured once: each replay is the next step, as without a graph."""
+    B, Hq, Hkv, D, page, steps = 5, 8, 2, 64, 4, 11
+    g = torch.Generator(device="cuda").manual_seed(12)
+    xs = torch.randn((steps, B, Hq + 2 * Hkv, D), generator=g, device="cuda").bfloat16()
+    freq, _ = lsa.rope_frequencies(D)
+    rope = lsa.Rope(freq.cuda())
+    add = i32([1, 1, 0, 1, 2])                      # row 2 waits; row 4 leaves a hole that later steps do not write
+
+    def run(captured):
+        pages = lsa.PageTable.empty(B, 8, B * 8, page)
+        k, v = (torch.zeros((B * 8, page, Hkv, D), device="cuda").to(DT[kind]) for _ in range(2))
+        ks, vs = (torch.ones((B * 8, page, Hkv), device="cuda") if kind == "e4m3" else None for _ in range(2))
+        cache = lsa.PageCache(k, v, ks, vs)
+        ws = torch.empty(lsa.paged_attn_workspace_size(cache, B, Hq), dtype=torch.uint8, device="cuda")
+        x, at = torch.empty_like(xs[0]), torch.empty_like(pages.len)
+        q, out = torch.empty((B, Hq, D), dtype=x.dtype, device="cuda"), torch.empty((B, Hq, D), dtype=x.dtype, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+        def step():
+            at.copy_(pages.len)
+            lsa.page_grow(pages, add, err)
+            at.masked_fill_(add == 0, -1)
+            lsa.qk_norm_rope(x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], q_out=q, pos=at, rope=rope, cache=cache,
+                             table=pages.table, at=at, err=err)
+            lsa.paged_attn(q, cache, pages.table, pages.len, out, ws, err=err)
+
+        got = []
+        if captured:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):              # loads the kernels
+                x.copy_(xs[0])
+                step()
+            torch.cuda.synchronize()
+            pages.table.fill_(-1)
+            pages.len.zero_()
+            pages.refs.zero_()
+            k.zero_(), v.zero_()
+            if ks is not None:
+                ks.fill_(1), vs.fill_(1)
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                step()
+        for i in range(steps):
+            x.copy_(xs[i])
+            graph.replay() if captured else step()
+            got.append(out.clone())
+        torch.cuda.synchronize()
+        assert err.item() == 0 and pages.len.tolist() == (steps * add).tolist()
+        return torch.stack(got), pages.table.clone(), k.view(torch.uint8).clone()
+
+    for a, b in zip(run(False), run(True)):
+        assert torch.equal(a, b)
