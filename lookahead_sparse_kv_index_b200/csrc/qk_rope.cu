@@ -14,9 +14,9 @@
 // rotation is four products a pair:
 //     a' = f (x_a (m w_a cos) - x_b (m w_b sin)),  b' = f (x_a (m w_a sin) + x_b (m w_b cos)),  f = 1 / sqrt(mean + eps).
 // The warp computes the token's angles once, reduced to a fraction of a turn in fp64 (pos * freq reaches millions of
-// radians, where fp32 keeps no fraction); only the fraction goes to the fp32 sincospi.  (Before that a CTA held the angles
-// of four tokens in shared memory and each row read them and its weights again: 380 instructions for four rows of 128,
-// and 99 us for 16384 tokens of 48 heads, bound by instruction issue.)
+// radians, where fp32 keeps no fraction); only the fraction goes to the fp32 sincospi, and its rounding is made good after.
+// (Before that a CTA held the angles of four tokens in shared memory and each row read them and its weights again: 380
+// instructions for four rows of 128, and 99 us for 16384 tokens of 48 heads, bound by instruction issue.)
 #include <math.h>
 
 #include "paged.cuh"
@@ -270,9 +270,13 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(QkArgs a) {
             __syncwarp();           // (the token before has read its angles)
             for (int i = wl; i < half; i += 32) {
                 const double turn = double(pos) * a.freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
+                // half turns; what rounding them to fp32 left turns the sine and cosine by as much (they would be off by
+                // up to pi 2^-25 else, more than by their own rounding)
+                const double h = 2.0 * (turn - rint(turn));
+                const float f = float(h), d = float(h - double(f)) * 3.14159265f;
                 float s, c;
-                sincospif(float(2.0 * (turn - rint(turn))), &s, &c);
-                cs[i] = make_float2(a.mscale * c, a.mscale * a.sign * s);
+                sincospif(f, &s, &c);
+                cs[i] = make_float2(a.mscale * fmaf(-s, d, c), a.mscale * a.sign * fmaf(c, d, s));
             }
             __syncwarp();
         }
