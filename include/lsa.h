@@ -401,11 +401,16 @@ typedef struct lsa_page_cache {
  * err       device error word or NULL.
  *           A wait inside a kernel that ran out (2 s) shows as LSA_ERR_TIMEOUT there;
  *           the call's outputs are then not to be used.
- * Products and sums are held in fp32 (E4M3 rows enter exactly, but for value rows
- * whose scale is below 2^-100, which lose low bits); each query's entries are
- * split over the device's SMs and joined in a fixed order, so the same call gives
- * the same bits.  One launch where a sequence's table holds few entries, else
- * two.
+ * Scores, weights and sums are held in fp32, and rows enter the products exactly.
+ * Rounded are: Q over an E4M3 cache, to f16 times a power of two of its head (exact
+ * down to 2^-28 of the head's largest element); and the softmax's weights where they
+ * multiply V: over BF16 rows to two bf16 numbers (off by 2^-16 of the weight), over
+ * E4M3 rows, times the row's scale, to one f16 number (off by 2^-11 of that product, or
+ * by 2^-34 of the largest product of the head's rows that are not all zeros; products
+ * below 2^-100 lose more).  An infinite element of a BF16 value row gives an infinity or
+ * NaN.  Each query's entries are split over the device's SMs and joined in a fixed
+ * order, so the same call gives the same bits.  One launch where a sequence's table
+ * holds few entries, else two.
  * ---------------------------------------------------------------------- */
 size_t lsa_paged_attn_workspace_size(const lsa_page_cache *cache, int32_t B, int32_t Hq);
 lsa_status lsa_paged_attn(const void *Q, lsa_dtype q_dtype, int64_t q_stride, const lsa_page_cache *cache,

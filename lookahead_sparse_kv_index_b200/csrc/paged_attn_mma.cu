@@ -17,16 +17,23 @@
 //     movmatrix transpose a tile.
 // Types.  bf16 rows are multiplied as they are.  e4m3 rows become f16 (exactly); q becomes f16 times a power of two of
 // its own head, which is exact for elements down to 2^-28 of the head's largest and off by less than 2^-38 of it below;
-// the scales of K multiply the fp32 scores, those of V the weights before they are rounded, relative to the largest
-// scale 2^R so far (o is rescaled when R grows, as it is when the running max does).
-// Weights.  A bf16 weight's rounding (2^-9) is as large as the output's own, and with one such number a weight the error
+// the scales of K multiply the fp32 scores, those of V the weights before they are rounded.
+// Weights.  A bf16 weight's rounding (2^-8) is as large as the output's own, and with one such number a weight the error
 // of the result is 1.4 times that of rounding it once; so what the rounding left is rounded too and multiplied as well
-// (2^-17 then).  An f16 weight's rounding (2^-12) is an eighth of the output's: one number does.
+// (2^-16 then).  An f16 weight's rounding (2^-11) is an eighth of the output's: one number does while it is a normal f16.
+// The range that leaves is kept around what counts: with p a row's softmax weight and s its V scale, p s enters times
+// 2^(9 - r), where 2^r is the power of two at or below a head's largest p s so far, less what the running max has moved
+// since.  It moves up (and o is rescaled) only when a product would pass 2^15, so products down to 2^-23 of the head's
+// largest are normal, and smaller ones off by at most 2^-34 of that.  Rows of zeros do not count as the largest: their
+// scale says nothing of a value.  (A reference that follows the scales alone, whatever the rows' weights, is lost to one
+// row of zeros at scale 1 among values of 1e-4.)
 //
-// Measured: 2 x 65536 entries of 8 bf16 heads of 128 under 64 query heads, 537 MB, 95 us, 5.7 TB/s (87% of the copy rate);
-// 64 sequences of up to 16384 entries, 479 MB, 88 us (84%).  The same bytes of e4m3 rows, 115 us (75%): twice the elements
-// a byte, each converted, permuted and multiplied, so instruction issue bounds it; 322 MB of ragged e4m3 contexts 73 us
-// (68%).
+// Measured: 2 x 65536 entries of 8 bf16 heads of 128 under 64 query heads, 537 MB, 96 us, 5.6 TB/s (86% of the copy rate);
+// 64 sequences of up to 16384 entries, 479 MB, 89 us (83%).  The same bytes of e4m3 rows, 118 us (72%): twice the elements
+// a byte, each converted, permuted and multiplied; 322 MB of ragged e4m3 contexts 75 us (66%).  Keeping the products'
+// range costs e4m3 rows 2 to 6% under up to 8 heads a kv head (two products and a maximum a weight), 9% under 16 and 18%
+// under 32, where registers spill (67 MB a head group of 8: 2 x 65536 entries of 128 under 16 heads 84 us, 2 x 32768
+// under 32 heads 104 us).
 #include <limits.h>
 
 #include "paged_attn.cuh"
@@ -141,6 +148,8 @@ struct Shape {
 
 constexpr int kMaxWarps = 4, kMaxStages = 4;
 constexpr float kLag = 8.f;
+constexpr uint32_t kMostFactor = 127 + 9 + 100;     // of e4m3 weights, as a biased exponent
+constexpr float kMostWeight = 32768.f;              // (f16 ends at 65504)
 
 template <bool E4M3, int KB, int NT>
 __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int stages) {
@@ -297,16 +306,26 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int
             for (int x = 0; x < 2; ++x) sf[nt][x] = E4M3 ? scale2 / q_scale[nt * 8 + 2 * c + x] : scale2;
 
         float m[NT][2], l[NT][2], o[C::kTiles][NT][4];
-        int R = -100;         // weights are held relative to scales of 2^R (e4m3)
+        uint32_t ge[NT][2];   // e4m3: biased exponent of 2^(9 - r), the factor of a head's weights (r >= -100)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = -INFINITY;
             l[nt][0] = l[nt][1] = 0.f;
+            ge[nt][0] = ge[nt][1] = kMostFactor;
 #pragma unroll
             for (int t = 0; t < C::kTiles; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[t][nt][e] = 0.f;
         }
+        auto rescale = [&](int nt, float f0, float f1) {
+#pragma unroll
+            for (int t = 0; t < C::kTiles; ++t) {
+                o[t][nt][0] *= f0;
+                o[t][nt][1] *= f1;
+                o[t][nt][2] *= f0;
+                o[t][nt][3] *= f1;
+            }
+        };
 
         for (int j = 0, now = 0, next = stages - 1; j < n; ++j) {
             cp_wait(stages - 2);
@@ -381,21 +400,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int
                         }
                 }
             }
-            int grown = 0;
-            if constexpr (E4M3) {
-                int e = -100;
-#pragma unroll
-                for (int tm = 0; tm < C::kM; ++tm)
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) e = max(e, int(__float_as_uint(vs[tm][y]) >> 23 & 255) - 127);
-                e = min(__reduce_max_sync(0xffffffffu, e), 127);
-                grown = e > R ? e - R : 0;
-                R += grown;
-                const float f = __uint_as_float(uint32_t(127 + 5 - R) << 23);   // 2^(5 - R): weights of up to 2^(5 + 8 + 1)
-#pragma unroll
-                for (int tm = 0; tm < C::kM; ++tm) vs[tm][0] *= f, vs[tm][1] *= f;
-            }
-            bool moved = grown != 0;
+            bool moved = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -404,7 +409,6 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int
                     for (int tm = 0; tm < C::kM; ++tm)
                         moved |= fmaxf(s[tm][nt][x], s[tm][nt][2 + x]) > m[nt][x] + kLag;
             if (__any_sync(0xffffffffu, moved)) {
-                const float f = E4M3 ? __uint_as_float(uint32_t(max(127 - grown, 0)) << 23) : 1.f;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float alpha[2];
@@ -416,18 +420,17 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                        alpha[x] = exp2_approx(m[nt][x] - (v == -INFINITY ? 0.f : v));
+                        const float fall = m[nt][x] - (v == -INFINITY ? 0.f : v);
+                        alpha[x] = exp2_approx(fall);
                         m[nt][x] = v;
                         l[nt][x] *= alpha[x];
-                        alpha[x] *= f;
+                        if constexpr (E4M3) {       // the reference of the products falls with the weights so far
+                            const uint32_t to = min(ge[nt][x] + uint32_t(fminf(ceilf(-fall), 256.f)), kMostFactor);
+                            alpha[x] = exp2_approx(fall + float(to - ge[nt][x]));
+                            ge[nt][x] = to;
+                        }
                     }
-#pragma unroll
-                    for (int t = 0; t < C::kTiles; ++t) {
-                        o[t][nt][0] *= alpha[0];
-                        o[t][nt][1] *= alpha[1];
-                        o[t][nt][2] *= alpha[0];
-                        o[t][nt][3] *= alpha[1];
-                    }
+                    rescale(nt, alpha[0], alpha[1]);
                 }
             }
             float ref[NT][2];
@@ -447,7 +450,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int
                         l[nt][0] += p0;
                         l[nt][1] += p1;
                         if constexpr (E4M3) {
-                            ph[tm][nt][y] = movmatrix(pack_f16(p0 * vs[tm][y], p1 * vs[tm][y]));
+                            s[tm][nt][2 * y] = p0 * vs[tm][y];
+                            s[tm][nt][2 * y + 1] = p1 * vs[tm][y];
                         } else {
                             uint32_t h, r;
                             split_bf16(p0, p1, h, r);
@@ -455,6 +459,62 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int
                             pl[tm][nt][y] = movmatrix(r);
                         }
                     }
+            if constexpr (E4M3) {
+                auto largest = [&](int nt, int x) {
+                    float v = 0.f;
+#pragma unroll
+                    for (int tm = 0; tm < C::kM; ++tm) v = fmaxf(v, fmaxf(fabsf(s[tm][nt][x]), fabsf(s[tm][nt][2 + x])));
+                    return v;
+                };
+                bool past = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) past |= largest(nt, x) * __uint_as_float(ge[nt][x] << 23) > kMostWeight;
+                if (__any_sync(0xffffffffu, past)) {
+                    // rows of zeros leave; of the others' products the largest is a head's new reference
+                    uint32_t bits = 0;
+#pragma unroll 1
+                    for (int p = lane / C::kStep; p < nch; p += 32 / C::kStep) {
+                        const uint4 v = lds16(sv + piece_at(lane % C::kStep, p));
+                        bits |= (v.x | v.y) | (v.z | v.w);
+                    }
+                    uint32_t some = __ballot_sync(0xffffffffu, (bits & 0x7f7f7f7fu) != 0);
+                    if (C::kStep == 16) some |= some >> 16;
+#pragma unroll
+                    for (int tm = 0; tm < C::kM; ++tm)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+                            if (!((some >> (tm * 16 + entry_of<E4M3>(g + 8 * y))) & 1u)) {
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) s[tm][nt][2 * y] = s[tm][nt][2 * y + 1] = 0.f;
+                            }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float f[2];
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            float v = largest(nt, x);
+                            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                            // 2^(9 - e) for a largest product of exponent e (e at most 127)
+                            const uint32_t to = min(ge[nt][x], 127 + 9 + 127 - min(__float_as_uint(v) >> 23, 254u));
+                            f[x] = __uint_as_float(uint32_t(max(127 - int(ge[nt][x] - to), 0)) << 23);
+                            ge[nt][x] = to;
+                        }
+                        rescale(nt, f[0], f[1]);
+                    }
+                }
+#pragma unroll
+                for (int tm = 0; tm < C::kM; ++tm)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+                            ph[tm][nt][y] = movmatrix(pack_f16(s[tm][nt][2 * y] * __uint_as_float(ge[nt][0] << 23),
+                                                               s[tm][nt][2 * y + 1] * __uint_as_float(ge[nt][1] << 23)));
+            }
             if constexpr (E4M3) {
 #pragma unroll
                 for (int p = 0; p < C::kPass; ++p) {
@@ -506,7 +566,6 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int
         }
         cp_wait(0);
         __syncthreads();      // the parts overlay every warp's stages
-        const float back = E4M3 ? __uint_as_float(uint32_t(127 - 5 + R) << 23) : 1.f;   // 2^(R - 5)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -521,6 +580,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_attn_mma(AttnArgs a, int
                     pml[(warp * C::kHeads + h) * 2 + 1] = L;
                 }
                 float *part = po + (size_t(warp) * C::kHeads + h) * D;
+                const float back = E4M3 ? __uint_as_float((254u - ge[nt][x]) << 23) : 1.f;      // 2^(r - 9)
 #pragma unroll
                 for (int t = 0; t < C::kTiles; ++t) {
                     if constexpr (E4M3) {
