@@ -448,7 +448,8 @@ lsa_status lsa_paged_attn(const void *Q, lsa_dtype q_dtype, int64_t q_stride, co
  *           table row seq[t] (row t if seq is NULL).  Tokens with a negative at or
  *           seq are not appended.  v is required unless the cache is latent (v ==
  *           k), where it must be NULL.  Rows of an E4M3 cache are rounded from
- *           fp32 with scale = max|y| / 448 (1 for a row of zeros).  No two tokens
+ *           fp32: scale = max|y| / 448 (at least 2^-126; 1 for a row of zeros), code =
+ *           y / scale.  No two tokens
  *           may name the same entry.  An entry outside the table (n_rows rows,
  *           max_pages * page_size entries) or on a page outside [0, n_pages) is not
  *           written and *err = LSA_ERR_INVALID.

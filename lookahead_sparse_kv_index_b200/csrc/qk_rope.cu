@@ -115,17 +115,28 @@ __device__ __forceinline__ void store_n(uint8_t *p, const float (&x)[N]) {
     }
 }
 
-// x * inv as e4m3 codes.
+// x / scale: one step of correction by the remainder makes the product with the rounded reciprocal `inv` the rounded
+// quotient (P. Markstein, IBM J. Res. Dev. 34, 1990).  Without it what lies on the middle between two codes goes either
+// way: 4 codes in 10000 of bf16 values.  (16384 tokens of 48 bf16 heads into e4m3 rows take 81 us, without the correction
+// 77, with a division an element 90.)  Remainders have to be normal numbers: the caller passes x and scale times a power
+// of two where scale is tiny.
+__device__ __forceinline__ float quotient(float x, float scale, float inv) {
+    const float q = x * inv;
+    return fmaf(fmaf(-q, scale, x), inv, q);
+}
+
+// x / scale as e4m3 codes.
 template <int N>
-__device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&x)[N], float inv) {
+__device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&x)[N], float up, float scale, float inv) {
     if constexpr (N == 1) {
-        *p = uint8_t(__nv_cvt_float_to_fp8(x[0] * inv, __NV_SATFINITE, __NV_E4M3));
+        *p = uint8_t(__nv_cvt_float_to_fp8(quotient(x[0] * up, scale, inv), __NV_SATFINITE, __NV_E4M3));
     } else {
         uint16_t c[N / 2];
 #pragma unroll
         for (int i = 0; i < N / 2; ++i)
-            c[i] = uint16_t(__nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * inv, x[2 * i + 1] * inv), __NV_SATFINITE,
-                                                     __NV_E4M3));
+            c[i] = uint16_t(__nv_cvt_float2_to_fp8x2(make_float2(quotient(x[2 * i] * up, scale, inv),
+                                                                 quotient(x[2 * i + 1] * up, scale, inv)),
+                                                     __NV_SATFINITE, __NV_E4M3));
         if constexpr (N == 8)
             *reinterpret_cast<uint2 *>(p) = make_uint2(c[0] | uint32_t(c[1]) << 16, c[2] | uint32_t(c[3]) << 16);
         else if constexpr (N == 4) *reinterpret_cast<uint32_t *>(p) = c[0] | uint32_t(c[1]) << 16;
@@ -407,13 +418,14 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(QkArgs a) {
                         for (int d = 16; d > 0; d >>= 1)
                             if (d < lpr) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
                         // (a row of tiny values keeps a normal scale, so that 0 / scale is 0)
-                        const float scale = amax > 0.f ? fmaxf(amax / 448.f, 1.17549435e-38f) : 1.f, inv = 1.f / scale;
+                        const float scale = amax > 0.f ? fmaxf(amax / 448.f, 1.17549435e-38f) : 1.f;
+                        const float up = scale < 0x1p-60f ? 0x1p64f : 1.f, su = scale * up, inv = 1.f / su;
                         if (on) {
 #pragma unroll
                             for (int m = 0; m < MU; ++m) {
                                 if (mine[m]) {
-                                    store_e4m3<VP>(cache + ia[m] / E, ya[m], inv);
-                                    store_e4m3<VP>(cache + ib[m] / E, yb[m], inv);
+                                    store_e4m3<VP>(cache + ia[m] / E, ya[m], up, su, inv);
+                                    store_e4m3<VP>(cache + ib[m] / E, yb[m], up, su, inv);
                                 }
                             }
                             if (lane == 0) (kind == 1 ? a.cache.ks : a.cache.vs)[slot * a.cache.Hkv + h] = scale;
