@@ -438,8 +438,9 @@ lsa_status lsa_paged_attn(const void *Q, lsa_dtype q_dtype, int64_t q_stride, co
  *           starts at element t * q_stride (k_stride, v_stride), so that they may
  *           be parts of one projection's output.  k NULL: queries only.
  * q_out, k_out  likewise; may be q and k themselves (same strides), and overlap
- *           nothing else of the call (refused).  k_out may be NULL where a cache
- *           takes the keys.
+ *           nothing else of the call: refused where rows share bytes, or where the
+ *           range from first row to last meets another operand than q, k, v, q_out and
+ *           k_out.  k_out may be NULL where a cache takes the keys.
  * q_weight, k_weight  [D] of `dtype`, or NULL (no norm of those heads).
  * pos       device int32 [T], required with rot_dim > 0.
  * rope      NULL: no rotation.  rope->freq: device fp64 [rot_dim / 2], radians per

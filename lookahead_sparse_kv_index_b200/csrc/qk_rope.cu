@@ -564,6 +564,24 @@ extern "C" lsa_status lsa_qk_norm_rope(const void *q, int64_t q_stride, void *q_
     } else {
         LSA_CHECK_ARG(!v, "lsa_qk_norm_rope: v goes to a cache");
     }
+    // nor may an output lie over what else the call reads or writes: it is enough that the ranges meet
+    const paged::Span rest[] = {
+        {q_weight, D * e, "q_weight"},
+        {k_weight, D * e, "k_weight"},
+        {rot ? pos : nullptr, T * 4, "pos"},
+        {rot ? rope->freq : nullptr, rot / 2 * 8, "freq"},
+        {cache ? cache->k : nullptr, cache ? paged::row_span(*cache) : 0, "the cache's keys"},
+        {cache ? cache->v : nullptr, cache ? paged::row_span(*cache) : 0, "the cache's values"},
+        {cache ? cache->k_scale : nullptr, cache ? paged::scale_span(*cache) : 0, "k_scale"},
+        {cache ? cache->v_scale : nullptr, cache ? paged::scale_span(*cache) : 0, "v_scale"},
+        {cache ? table : nullptr, cache ? paged::table_span(n_rows, table_stride, max_pages) : 0, "table"},
+        {cache ? seq : nullptr, T * 4, "seq"},
+        {cache ? at : nullptr, T * 4, "at"},
+        {err, 4, "err"}};
+    for (int o = 1; o < 5; o += 2)
+        for (const auto &x : rest)
+            LSA_CHECK_ARG(!paged::meet({in[o].p, ((T - 1) * in[o].stride + int64_t(in[o].heads) * D) * e, in[o].name}, x),
+                          "lsa_qk_norm_rope: %s overlaps %s", in[o].name, x.name);
 
     a.q = static_cast<const uint8_t *>(q);
     a.k = static_cast<const uint8_t *>(k);
