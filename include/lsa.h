@@ -389,6 +389,8 @@ typedef struct lsa_page_cache {
  * Q         [B, Hq, D]: F32 with an F32 cache, BF16 with a BF16 or E4M3 one;
  *           sequence b starts at element b * q_stride.
  * out       [B, Hq, D] of Q's type, contiguous.   lse  [B, Hq] fp32 or NULL.
+ *           out may be Q itself (q_stride = Hq * D); what the call writes (out, lse, the
+ *           workspace, err) shares no other byte with its operands (refused).
  * table     device int32, row b of max_pages page indices at b * table_stride;
  *           max_pages * page_size at most 2^30.
  * seq_len   device int32 [B].  Below 0 counts as 0; above max_pages * page_size

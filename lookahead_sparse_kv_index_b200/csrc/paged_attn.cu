@@ -201,6 +201,30 @@ extern "C" lsa_status lsa_paged_attn(const void *Q, lsa_dtype q_dtype, int64_t q
     LSA_CHECK_ARG(ws_bytes >= workspace_bytes(p, cache->D) && aligned16(workspace),
                   "lsa_paged_attn: workspace of %zu bytes < %zu", ws_bytes, workspace_bytes(p, cache->D));
 
+    // what a call writes lies apart from all else of it, but for an output in place of the queries: each head's is written
+    // when no one reads its query any more
+    const int64_t heads_bytes = int64_t(Hq) * cache->D * e;
+    const Span read[] = {{Q, (B - 1) * q_stride * e + heads_bytes, "Q"},
+                         {cache->k, row_span(*cache), "the cache's keys"},
+                         {cache->v, row_span(*cache), "the cache's values"},
+                         {cache->k_scale, scale_span(*cache), "k_scale"},
+                         {cache->v_scale, scale_span(*cache), "v_scale"},
+                         {table, table_span(B, table_stride, max_pages), "table"},
+                         {seq_len, int64_t(B) * 4, "seq_len"}};
+    const Span written[] = {{out, B * heads_bytes, "out"},
+                            {lse, int64_t(B) * Hq * 4, "lse"},
+                            {workspace, int64_t(workspace_bytes(p, cache->D)), "the workspace"},
+                            {err, 4, "err"}};
+    for (int w = 0; w < 4; ++w) {
+        for (const Span &x : read) {
+            const bool in_place = w == 0 && x.p == Q && out == Q && (B == 1 || q_stride == int64_t(Hq) * cache->D);
+            LSA_CHECK_ARG(in_place || !meet(written[w], x), "lsa_paged_attn: %s overlaps %s", written[w].name, x.name);
+        }
+        for (int i = 0; i < w; ++i)
+            LSA_CHECK_ARG(!meet(written[w], written[i]), "lsa_paged_attn: %s overlaps %s", written[w].name,
+                          written[i].name);
+    }
+
     AttnArgs a = {};
     a.cache = view_of(*cache);
     a.q = Q;

@@ -1,4 +1,6 @@
 """Calls of the paged-cache operators whose operands share memory are refused on the host (no CUDA call is reached)."""
+import ctypes
+
 import pytest
 
 from test_paged_cpu import BIG, _cache, _qk
@@ -31,3 +33,26 @@ def test_norm_rope_rejects_outputs_over_what_else_it_reads_or_writes(lsa):
     assert lsa.lib.lsa_qk_norm_rope(a["q"], 256, a["qo"], 256, None, 0, None, 0, None, 0, lsa.BF16, 5, 4, 0, 64, None, None,
                                     1e-6, None, None, None, None, 0, 0, 0, None, None, 2 * BIG + 4 * 256, None) == 1
     assert b"overlaps err" in lsa.lib.lsa_last_error()
+
+
+def test_attention_rejects_outputs_over_its_operands(lsa):
+    """out may be Q itself; any other shared byte of out, lse, the workspace and the error word is refused."""
+    c = _cache(lsa, dtype=lsa.E4M3, k=30 * BIG, v=31 * BIG, k_scale=32 * BIG, v_scale=33 * BIG)
+    span = 9 * c.page_stride + 15 * c.slot_stride + c.head_stride + 64           # bytes of the cache's keys
+    need = lsa.lib.lsa_paged_attn_workspace_size(ctypes.byref(c), 3, 4)
+    row, out_bytes = 4 * 64 * 2, 3 * 4 * 64 * 2
+    assert 0 < need < 16 * BIG
+    a = dict(Q=BIG, table=2 * BIG, sl=3 * BIG, out=4 * BIG, lse=5 * BIG, ws=8 * BIG, wsb=need, err=7 * BIG)
+
+    def call(**kw):
+        x = {**a, "qs": 4 * 64, **kw}
+        return lsa.lib.lsa_paged_attn(x["Q"], lsa.BF16, x["qs"], ctypes.byref(c), x["table"], 8, 8, x["sl"], 3, 4, 0, 1.0,
+                                      x["out"], x["lse"], x["ws"], x["wsb"], x["err"], None)
+
+    for kw in (dict(out=BIG + 16), dict(out=BIG - out_bytes + 16), dict(out=BIG, qs=5 * 64), dict(out=2 * BIG),
+               dict(out=2 * BIG + 3 * 8 * 4 - 16), dict(out=3 * BIG), dict(out=30 * BIG), dict(out=31 * BIG + span - 16),
+               dict(out=32 * BIG), dict(out=33 * BIG), dict(lse=4 * BIG + out_bytes - 4), dict(lse=BIG + row), dict(lse=3 * BIG),
+               dict(ws=BIG), dict(ws=4 * BIG), dict(ws=BIG - need + 16), dict(ws=5 * BIG), dict(out=8 * BIG + need // 32 * 16),
+               dict(ws=2 * BIG), dict(ws=33 * BIG), dict(err=4 * BIG), dict(err=8 * BIG + need - 4), dict(err=3 * BIG + 8)):
+        assert call(**kw) == 1, kw
+        assert b"overlaps" in lsa.lib.lsa_last_error(), kw
