@@ -509,6 +509,8 @@ lsa_status lsa_rope_frequencies(lsa_rope_kind kind, int32_t rot_dim, double base
  * is not empty, is named twice or is a src too), *err = LSA_ERR_INVALID; and the
  * books stay as they are (and a fork's list of copies is empty).  Page indices
  * outside [0, n_pages) in the books are never followed.
+ * The lists of a fork, a free and a packing lie apart from the books and, where they are
+ * written, from each other (refused), but for packing in place.
  * Limits: n_rows <= 65536, n_pages <= 2^24, max_pages * page_size < 2^31.  `err` may
  * be NULL.
  * ---------------------------------------------------------------------- */

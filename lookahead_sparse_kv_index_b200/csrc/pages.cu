@@ -13,6 +13,7 @@ namespace lsa {
 namespace {
 
 using paged::CacheView;
+using paged::Span;
 
 constexpr int kBooks = 1024;            // threads of a books kernel
 constexpr int kPer = 16;                // counts a thread and round
@@ -551,6 +552,27 @@ lsa_status check_books(const lsa_page_table *pt, const char *who, Books *bk) {
     return LSA_OK;
 }
 
+struct BookSpans {
+    Span s[3];
+};
+BookSpans book_spans(const Books &bk) {
+    return {{{bk.table, int64_t(bk.n_rows) * bk.max_pages * 4, "the table"},
+             {bk.len, int64_t(bk.n_rows) * 4, "len"},
+             {bk.refs, bk.n_pages * 4, "refs"}}};
+}
+
+// Refuses a call whose lists share bytes with each other (a call's inputs, the first `inputs` of them, may) or the books.
+template <int N>
+lsa_status check_apart(const Span (&x)[N], int inputs, const Books &bk, const char *who) {
+    for (int i = 0; i < N; ++i) {
+        for (const Span &b : book_spans(bk).s)
+            LSA_CHECK_ARG(!meet(x[i], b), "%s: %s overlaps %s", who, x[i].name, b.name);
+        for (int j = 0; j < i; ++j)
+            LSA_CHECK_ARG(i < inputs || !meet(x[i], x[j]), "%s: %s overlaps %s", who, x[i].name, x[j].name);
+    }
+    return LSA_OK;
+}
+
 int64_t pack_blocks(int64_t n_pages) { return (n_pages + kPackPages - 1) / kPackPages; }
 
 }  // namespace
@@ -578,6 +600,10 @@ extern "C" lsa_status lsa_page_fork(const lsa_page_table *pt, const int32_t *src
     LSA_CHECK_ARG(n >= 0 && n <= pt->n_rows, "lsa_page_fork: n=%d not in [0, n_rows]", n);
     if (n == 0) return LSA_OK;
     LSA_CHECK_ARG(src && dst && copy_src && copy_dst, "lsa_page_fork: src, dst, copy_src and copy_dst are required");
+    const Span lists[] = {{src, int64_t(n) * 4, "src"}, {dst, int64_t(n) * 4, "dst"}, {copy_src, int64_t(n) * 4, "copy_src"},
+                          {copy_dst, int64_t(n) * 4, "copy_dst"}};
+    const lsa_status apart = check_apart(lists, 2, bk, "lsa_page_fork");
+    if (apart != LSA_OK) return apart;
     cudaStream_t st = as_stream(stream);
     LSA_CUDA(launch_pdl(page_fork_take, dim3(1), dim3(kBooks), 0, st, bk, src, dst, int(n), copy_src, copy_dst, err));
     LSA_LAUNCHED("page_fork_take");
@@ -595,6 +621,9 @@ extern "C" lsa_status lsa_page_free(const lsa_page_table *pt, const int32_t *row
     LSA_CHECK_ARG(n >= 0, "lsa_page_free: n=%d < 0", n);
     if (n == 0) return LSA_OK;
     LSA_CHECK_ARG(rows, "lsa_page_free: rows is required");
+    const Span lists[] = {{rows, int64_t(n) * 4, "rows"}};
+    const lsa_status apart = check_apart(lists, 1, bk, "lsa_page_free");
+    if (apart != LSA_OK) return apart;
     LSA_CUDA(launch_pdl(page_free, dim3(n), dim3(kFork), 0, as_stream(stream), bk, rows, err));
     LSA_LAUNCHED("page_free");
     return LSA_OK;
@@ -617,6 +646,16 @@ extern "C" lsa_status lsa_page_compact(const lsa_page_table *pt, int32_t *table_
     LSA_CHECK_ARG(ws_bytes >= lsa_page_compact_workspace_size(pt->n_pages) && aligned16(workspace),
                   "lsa_page_compact: workspace of %zu bytes < %zu", ws_bytes,
                   lsa_page_compact_workspace_size(pt->n_pages));
+    // in place: the table and the counts as they are; anything else lies apart
+    const int64_t table_bytes = int64_t(pt->n_rows) * pt->max_pages * 4, page_bytes = pt->n_pages * 4;
+    const Span lists[] = {{table_out == pt->table ? nullptr : table_out, table_bytes, "table_out"},
+                          {refs_out == pt->refs ? nullptr : refs_out, page_bytes, "refs_out"},
+                          {move_src, page_bytes, "move_src"},
+                          {move_dst, page_bytes, "move_dst"},
+                          {n_moves, 4, "n_moves"},
+                          {workspace, int64_t(lsa_page_compact_workspace_size(pt->n_pages)), "the workspace"}};
+    const lsa_status apart = check_apart(lists, 0, bk, "lsa_page_compact");
+    if (apart != LSA_OK) return apart;
     const int blocks = int(pack_blocks(pt->n_pages));
     int32_t *cnt = static_cast<int32_t *>(workspace);
     int32_t *rank = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + align_up(size_t(blocks) * 4, 256));

@@ -3,7 +3,7 @@ import ctypes
 
 import pytest
 
-from test_paged_cpu import BIG, _cache, _qk
+from test_paged_cpu import BIG, _books, _cache, _qk
 
 
 @pytest.fixture(scope="module")
@@ -56,3 +56,24 @@ def test_attention_rejects_outputs_over_its_operands(lsa):
                dict(ws=2 * BIG), dict(ws=33 * BIG), dict(err=4 * BIG), dict(err=8 * BIG + need - 4), dict(err=3 * BIG + 8)):
         assert call(**kw) == 1, kw
         assert b"overlaps" in lsa.lib.lsa_last_error(), kw
+
+
+def test_page_calls_reject_lists_over_each_other_and_the_books(lsa):
+    """What a call writes may not be what it reads elsewhere; packing in place means the whole table, the whole counts."""
+    L = lsa.lib
+    b = _books(lsa, table=BIG, len=2 * BIG, refs=3 * BIG)                        # 4 rows of 8 pages, 100 pages
+    refused = lambda status: status == 1 and b"overlaps" in L.lsa_last_error()   # noqa: E731
+    fork = dict(src=4 * BIG, dst=5 * BIG, cs=6 * BIG, cd=7 * BIG)
+    for kw in (dict(cs=4 * BIG), dict(cs=5 * BIG + 4), dict(cd=4 * BIG + 4), dict(cd=6 * BIG), dict(cs=BIG + 124),
+               dict(cd=2 * BIG), dict(cs=3 * BIG + 396), dict(src=BIG), dict(dst=2 * BIG + 8), dict(src=3 * BIG)):
+        x = {**fork, **kw}
+        assert refused(L.lsa_page_fork(b, x["src"], x["dst"], 2, x["cs"], x["cd"], None, None)), kw
+    for rows in (BIG, 2 * BIG + 12, 3 * BIG + 200):
+        assert refused(L.lsa_page_free(b, rows, 3, None, None)), rows
+    size = lsa.page_compact_workspace_size(100)
+    pack = dict(t=4 * BIG, r=5 * BIG, ms=6 * BIG, md=7 * BIG, n=8 * BIG, ws=9 * BIG)
+    for kw in (dict(t=BIG + 4), dict(r=3 * BIG + 4), dict(r=BIG), dict(t=3 * BIG), dict(t=2 * BIG), dict(ms=BIG), dict(md=3 * BIG),
+               dict(ms=2 * BIG), dict(md=6 * BIG + 396), dict(n=6 * BIG), dict(n=2 * BIG), dict(ws=3 * BIG), dict(ws=BIG),
+               dict(ws=4 * BIG), dict(ms=9 * BIG + size - 4), dict(r=4 * BIG + 64)):
+        x = {**pack, **kw}
+        assert refused(L.lsa_page_compact(b, x["t"], x["r"], x["ms"], x["md"], x["n"], x["ws"], size, None)), kw
