@@ -283,6 +283,12 @@ def _need(ok, what):
         raise ValueError(what)
 
 
+def _fits(x, name):
+    """Refuses a number that an int32 argument would take modulo 2^32."""
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{name}={x} is no int32")
+
+
 def _i32(t, name, device, *shape):
     """The address of a contiguous int32 tensor of `shape` on `device`."""
     if t.dtype is not _I32 or t.device != device or t.shape != shape or not t.is_contiguous():
@@ -356,6 +362,8 @@ class PageCache:
 
 def paged_attn_workspace_size(cache, B, Hq) -> int:
     """Bytes of paged_attn's workspace on the cache's device (raises on heads that the library does not run)."""
+    _fits(B, "B")
+    _fits(Hq, "Hq")
     if cache.device.type != "cuda" or cache.device.index == torch._C._cuda_getDevice():
         n = _L.lsa_paged_attn_workspace_size(cache._ref, B, Hq)
     else:
@@ -395,6 +403,7 @@ def paged_attn(Q, cache, table, seq_len, out, workspace, lse=None, window=0, sca
     """
     dev, dtype = cache.device, Q.dtype
     B, Hq, D = Q.shape
+    _fits(window, "window")
     if dtype not in _ELEM:
         raise ValueError(f"Q: float32 or bfloat16 is needed, not {dtype}")
     qp, qs = _heads(Q, "Q", B, Hq, cache.D, dtype, dev)
@@ -419,6 +428,7 @@ ROPE_KINDS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
 def rope_frequencies(rot_dim, base=10000.0, kind="plain", factor=1.0, orig_len=0, beta_fast=32.0, beta_slow=1.0):
     """(frequencies float64 [rot_dim / 2] on the host, mscale) of a plain or scaled rotation (lsa_rope_frequencies)."""
     _need(kind in ROPE_KINDS, f"kind: one of {', '.join(ROPE_KINDS)} is needed, not {kind!r}")
+    _fits(rot_dim, "rot_dim")
     freq, m = torch.empty(max(1, rot_dim // 2), dtype=torch.float64), ctypes.c_float()
     _check(_L.lsa_rope_frequencies(ROPE_KINDS[kind], rot_dim, base, factor, orig_len, beta_fast, beta_slow,
                                    freq.data_ptr(), ctypes.byref(m)), "lsa_rope_frequencies")
@@ -491,6 +501,7 @@ class PageTable:
     def __init__(self, table, length, refs, page_size):
         _need(table.dim() == 2 and refs.dim() == 1, "table: [n_rows, max_pages] and refs: [n_pages] are needed")
         self.table, self.len, self.refs, self.page_size = table, length, refs, int(page_size)
+        _fits(self.page_size, "page_size")
         self.device = table.device
         self.n_rows, self.max_pages = table.shape
         self.n_pages = refs.numel()

@@ -1,7 +1,9 @@
-"""Calls of the paged-cache operators whose operands share memory are refused on the host (no CUDA call is reached)."""
+"""Calls of the paged-cache operators that are refused on the host (no CUDA call is reached): operands that share memory,
+numbers that a C type would cut."""
 import ctypes
 
 import pytest
+import torch
 
 from test_paged_cpu import BIG, _books, _cache, _qk
 
@@ -77,3 +79,22 @@ def test_page_calls_reject_lists_over_each_other_and_the_books(lsa):
                dict(ws=4 * BIG), dict(ms=9 * BIG + size - 4), dict(r=4 * BIG + 64)):
         x = {**pack, **kw}
         assert refused(L.lsa_page_compact(b, x["t"], x["r"], x["ms"], x["md"], x["n"], x["ws"], size, None)), kw
+
+
+def test_bindings_refuse_numbers_that_their_types_would_cut(lsa):
+    """ctypes takes an int32 modulo 2^32: a window of 2^32 + 5 would be one of 5."""
+    cache = lsa.PageCache(torch.zeros((4, 8, 2, 32)))
+    q, i = torch.zeros((3, 4, 32)), torch.zeros(3, dtype=torch.int32)
+    table, ws = torch.zeros((3, 5), dtype=torch.int32), torch.zeros(1 << 10)
+    for window in (1 << 31, (1 << 32) + 5, -(1 << 32)):
+        with pytest.raises(ValueError, match="window"):
+            lsa.paged_attn(q, cache, table, i, q.clone(), ws, window=window)
+    for size in (1 << 31, (1 << 32) + 16):
+        with pytest.raises(ValueError, match="page_size"):
+            lsa.PageTable(table, i, i, size)
+    with pytest.raises(ValueError, match="rot_dim"):
+        lsa.rope_frequencies((1 << 32) + 64)
+    with pytest.raises(ValueError, match="B="):
+        lsa.paged_attn_workspace_size(cache, (1 << 32) + 1, 4)
+    with pytest.raises(ValueError, match="Hq="):
+        lsa.paged_attn_workspace_size(cache, 1, (1 << 32) + 4)
