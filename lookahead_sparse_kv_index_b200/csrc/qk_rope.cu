@@ -34,8 +34,7 @@ struct QkArgs {
     uint8_t *q_out, *k_out;
     int64_t q_stride, q_out_stride, k_stride, k_out_stride, v_stride;   // bytes between tokens
     int32_t row_bytes;           // of a head of q, k, v
-    int64_t T;
-    int32_t Hq, Hkv, D, rot, interleaved;
+    int32_t Hq, Hkv, D, rot;
     float sign, mscale, eps, inv_d;
     const uint8_t *wq, *wk;
     const int32_t *pos;
@@ -47,11 +46,15 @@ struct QkArgs {
     int32_t n_rows;
     int64_t reach;
     int32_t *err;
-    int32_t mixed;               // 1: parts hold whole pairs, some of which may turn
     int32_t lpr;                 // lanes of a row, a power of two
     int32_t nq, nk, nv;          // rounds of a token's queries, keys, values: 32 / lpr rows each
     int64_t share, spare;        // rounds of a warp; the first `spare` warps have one more
     int64_t warps;
+};
+// What chooses the kernel besides.
+struct QkForm {
+    bool interleaved;
+    bool mixed;                  // parts hold whole pairs, some of which may turn
 };
 
 // N consecutive elements as they lie in memory, and in fp32.
@@ -162,22 +165,22 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(QkArgs a) {
 
     // A unit's two parts of VP elements: byte offsets, and its first pair (of each part, where the parts hold whole pairs;
     // `turns`: whether they turn).  Lanes are neighbours in both parts, so that their accesses fill whole sectors.
-    constexpr bool kWhole = IL && VP > 1;
-    static_assert(kWhole || !MIX, "parts of halves of pairs turn as one");
+    static_assert(!IL || VP * E == 16, "interleaved pairs always go by whole 16 bytes");
+    static_assert(IL || !MIX, "parts of halves of pairs turn as one");
     int ia[MU], ib[MU], pa[MU], pb[MU];
     bool mine[MU], turns[MU][MIX ? VP : 2];
 #pragma unroll
     for (int m = 0; m < MU; ++m) {
         const int u = lane + lpr * m, p = u * VP;
         mine[m] = u < U;
-        if (kWhole) {
+        if (IL) {
             ia[m] = p * E;
             ib[m] = (p + a.D / 2) * E;
             pa[m] = p / 2;
             pb[m] = (p + a.D / 2) / 2;
         } else {
-            ia[m] = (IL ? 2 * p : p < half ? p : a.rot + (p - half)) * E;
-            ib[m] = (IL ? 2 * p + 1 : p < half ? p + half : a.rot + rest + (p - half)) * E;
+            ia[m] = (p < half ? p : a.rot + (p - half)) * E;
+            ib[m] = (p < half ? p + half : a.rot + rest + (p - half)) * E;
             pa[m] = pb[m] = p;
         }
         if constexpr (MIX) {
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(QkArgs a) {
                     }
 #pragma unroll
                     for (int e = 0; e < VP; ++e) {
-                        const int second = kWhole && e >= VP / 2;
+                        const int second = IL && e >= VP / 2;
                         const float2 c = turns[m][MIX ? e : second] ? cs[second ? pb[m] + e - VP / 2 : pa[m] + e] : make_float2(1.f, 0.f);
                         const float u = IL ? wt[2 * e] : wt[e], v = IL ? wt[2 * e + 1] : wt[VP + e];
                         ac[m][e] = u * c.x;
@@ -371,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(QkArgs a) {
                         for (int e = 0; e < VP; ++e) {
                             float &x0 = x[m][IL ? 2 * e : e], &x1 = x[m][IL ? 2 * e + 1 : VP + e];
                             float p = x0 * ac[m][e], q = x1 * bc[m][e];
-                            if (turns[m][MIX ? e : kWhole && e >= VP / 2]) {       // (an element that does not turn never meets its partner)
+                            if (turns[m][MIX ? e : IL && e >= VP / 2]) {       // (an element that does not turn never meets its partner)
                                 p = fmaf(-x1, bs[m][e], p);
                                 q = fmaf(x0, as[m][e], q);
                             }
@@ -446,36 +449,61 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope(QkArgs a) {
     }
 }
 
-template <typename T, int VP, int MU, int LPR, bool MIX = false>
+template <typename T, int VP, int MU, int LPR, bool IL, bool MIX = false>
 lsa_status launch_as(const QkArgs &a, unsigned grid, cudaStream_t st) {
     const size_t smem = size_t(kWarps) * (size_t(kAhead) * 32 * 2 * MU * VP * sizeof(T) + size_t(a.rot / 2) * 8);
-    auto *kernel = a.interleaved ? qk_norm_rope<T, VP, MU, LPR, true, MIX> : qk_norm_rope<T, VP, MU, LPR, MIX, MIX>;
+    auto *kernel = qk_norm_rope<T, VP, MU, LPR, IL, MIX>;
     LSA_CUDA(ensure_smem(kernel, smem));
     LSA_CUDA(launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, st, a));
     LSA_LAUNCHED("qk_norm_rope");
     return LSA_OK;
 }
-// The usual head dims have the lanes of a row at compile time (64, 128 and 256 elements at the widest unit).
+// Units of 16-byte parts: the usual head dims have the lanes of a row at compile time (64, 128 and 256 elements).
+template <typename T, bool IL>
+lsa_status launch_wide(const QkArgs &a, bool mixed, unsigned grid, cudaStream_t st) {
+    constexpr int VP = 16 / int(sizeof(T)), kRow = 128 / 2 / VP, kMost = 8 / VP;    // units of a lane: 2 (fp32) or 1
+    const int units = (a.D / 2 / VP + a.lpr - 1) / a.lpr;
+    if constexpr (IL) {
+        if constexpr (kMost > 1)
+            if (mixed && units > 1) return launch_as<T, VP, kMost, 0, IL, true>(a, grid, st);
+        if (mixed) return launch_as<T, VP, 1, 0, IL, true>(a, grid, st);
+    }
+    if constexpr (kMost > 1)
+        if (units > 1) return launch_as<T, VP, kMost, 0, IL>(a, grid, st);
+    if (a.lpr == kRow / 2) return launch_as<T, VP, 1, kRow / 2, IL>(a, grid, st);
+    if (a.lpr == kRow) return launch_as<T, VP, 1, kRow, IL>(a, grid, st);
+    if (a.lpr == 2 * kRow) return launch_as<T, VP, 1, 2 * kRow, IL>(a, grid, st);
+    return launch_as<T, VP, 1, 0, IL>(a, grid, st);
+}
+// Narrower ones, of halves of pairs alone.
 template <typename T, int VP>
 lsa_status launch_vp(const QkArgs &a, unsigned grid, cudaStream_t st) {
     const int units = (a.D / 2 / VP + a.lpr - 1) / a.lpr;    // of a lane: at most 8 / VP
-    if constexpr (VP * sizeof(T) == 16) {
-        constexpr int kRow = 128 / 2 / VP;
-        if (a.mixed) {
-            if (units == 1) return launch_as<T, VP, 1, 0, true>(a, grid, st);
-            return launch_as<T, VP, 2, 0, true>(a, grid, st);
-        }
-        if (a.lpr == kRow / 2) return launch_as<T, VP, 1, kRow / 2>(a, grid, st);
-        if (a.lpr == kRow) return launch_as<T, VP, 1, kRow>(a, grid, st);
-        if (a.lpr == 2 * kRow && units == 1) return launch_as<T, VP, 1, 2 * kRow>(a, grid, st);
-    }
-    if (units == 1) return launch_as<T, VP, 1, 0>(a, grid, st);
+    if (units == 1) return launch_as<T, VP, 1, 0, false>(a, grid, st);
     if constexpr (VP <= 1)
-        if (units > 4) return launch_as<T, VP, 8, 0>(a, grid, st);
+        if (units > 4) return launch_as<T, VP, 8, 0, false>(a, grid, st);
     if constexpr (VP <= 2)
-        if (units > 2) return launch_as<T, VP, 4, 0>(a, grid, st);
-    if constexpr (VP <= 4) return launch_as<T, VP, 2, 0>(a, grid, st);
-    return launch_as<T, VP, 1, 0>(a, grid, st);
+        if (units > 2) return launch_as<T, VP, 4, 0, false>(a, grid, st);
+    return launch_as<T, VP, 2, 0, false>(a, grid, st);
+}
+lsa_status launch_form(const QkArgs &a, const QkForm &f, int vp, unsigned grid, cudaStream_t st, bool bf16) {
+    if (bf16) {
+        switch (vp) {
+        case 8:
+            return f.interleaved ? launch_wide<uint16_t, true>(a, f.mixed, grid, st)
+                                 : launch_wide<uint16_t, false>(a, false, grid, st);
+        case 4: return launch_vp<uint16_t, 4>(a, grid, st);
+        case 2: return launch_vp<uint16_t, 2>(a, grid, st);
+        default: return launch_vp<uint16_t, 1>(a, grid, st);
+        }
+    }
+    switch (vp) {
+    case 4:
+        return f.interleaved ? launch_wide<float, true>(a, f.mixed, grid, st)
+                             : launch_wide<float, false>(a, false, grid, st);
+    case 2: return launch_vp<float, 2>(a, grid, st);
+    default: return launch_vp<float, 1>(a, grid, st);
+    }
 }
 
 // Whether two arrays of T rows share bytes (rows `as` and `bs` bytes apart, `aw` and `bw` wide).  Of arrays with different
@@ -593,12 +621,12 @@ extern "C" lsa_status lsa_qk_norm_rope(const void *q, int64_t q_stride, void *q_
     a.k_stride = k_stride * e;
     a.k_out_stride = k_out_stride * e;
     a.v_stride = v_stride * e;
-    a.T = T;
     a.Hq = Hq;
     a.Hkv = k ? Hkv : 0;
     a.D = D;
     a.rot = rot;
-    a.interleaved = rot == 0 || rope->interleaved;   // without a rotation, the layout with the wider accesses
+    QkForm form = {};
+    form.interleaved = rot == 0 || rope->interleaved;   // without a rotation, the layout with the wider accesses
     a.sign = rope && rope->inverse ? -1.f : 1.f;
     a.mscale = rope && rope->mscale != 0.f ? rope->mscale : 1.f;
     a.eps = eps;
@@ -619,8 +647,8 @@ extern "C" lsa_status lsa_qk_norm_rope(const void *q, int64_t q_stride, void *q_
     // units of one pair): a kernel of its own, since the flags cost a few instructions.
     int vp = dtype == LSA_BF16 ? 8 : 4;
     auto fits = [&](int n) { return rot / 2 % n == 0 && (D - rot) / 2 % n == 0; };
-    a.mixed = a.interleaved && !fits(vp);
-    while (!a.mixed && !fits(vp)) vp /= 2;
+    form.mixed = form.interleaved && !fits(vp);
+    while (!form.mixed && !fits(vp)) vp /= 2;
     a.lpr = 1;
     while (a.lpr < 32 && a.lpr * vp < D / 2) a.lpr *= 2;
     const int groups = 32 / a.lpr;
@@ -635,19 +663,7 @@ extern "C" lsa_status lsa_qk_norm_rope(const void *q, int64_t q_stride, void *q_
     a.spare = total - a.share * a.warps;
     const unsigned grid = unsigned((a.warps + kWarps - 1) / kWarps);
     cudaStream_t st = as_stream(stream);
-    if (dtype == LSA_BF16) {
-        switch (vp) {
-        case 8: return launch_vp<uint16_t, 8>(a, grid, st);
-        case 4: return launch_vp<uint16_t, 4>(a, grid, st);
-        case 2: return launch_vp<uint16_t, 2>(a, grid, st);
-        default: return launch_vp<uint16_t, 1>(a, grid, st);
-        }
-    }
-    switch (vp) {
-    case 4: return launch_vp<float, 4>(a, grid, st);
-    case 2: return launch_vp<float, 2>(a, grid, st);
-    default: return launch_vp<float, 1>(a, grid, st);
-    }
+    return launch_form(a, form, vp, grid, st, dtype == LSA_BF16);
 }
 
 extern "C" lsa_status lsa_rope_frequencies(lsa_rope_kind kind, int32_t rot_dim, double base, double factor,
