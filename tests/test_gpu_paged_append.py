@@ -47,3 +47,29 @@ def test_e4m3_codes_are_the_rounded_quotients(lsa, dtype, T, Hkv, D, rot, interl
             a, b = codes[order, 0].cpu().view(torch.uint8), want.view(torch.uint8)
             zero = ((a | b) & 0x7F) == 0                      # (a rotation by 0 may turn -0 into 0)
             assert ((a == b) | zero).all(), f"{int(((a != b) & ~zero).sum())} of {a.numel()} codes differ"
+
+
+@pytest.mark.parametrize("inverse", [False, True])
+def test_the_angle_is_not_rounded_to_fp32(lsa, inverse):
+    """Angles next to half a turn, where the sine is small and shows the angle's own error.  An odd position times
+    freq = pi (1 - u) is a turn's half less pos u pi, |sin| < 2^-5: off by a unit of sincospi and half a step of its
+    correction by what the angle's rounding left, 1.5 * 2^-29 (and 2^-45 of the fp64 angle): 2^-28 bounds it.  Half turns
+    rounded to fp32 alone are off by up to 2^-25, the sine by up to pi 2^-25, eleven times the bound."""
+    T, half = 257, 64
+    r = np.random.default_rng(0)
+    pos = 2 * r.integers(0, 40, T) + 1
+    u = r.uniform(0, 2.0 ** -5 / 4 / 81, half)
+    freq = np.pi * (1 - u)
+    x = torch.zeros((T, 1, 2 * half), device="cuda")
+    x[:, :, :half] = 1                                    # (1, 0) turns to (cos, sin)
+    out = torch.empty_like(x)
+    lsa.qk_norm_rope(x, q_out=out, pos=i32(pos), rope=lsa.Rope(torch.from_numpy(freq).cuda(), inverse=inverse))
+    got = out[:, 0, half:].double().cpu().numpy()
+    phi = pos[:, None] * freq * (-1.0 if inverse else 1.0)
+    want = np.sin(phi)
+    assert np.abs(want).max() < 2.0 ** -5
+    assert np.abs(got - want).max() <= 2.0 ** -28
+    assert np.abs(out[:, 0, :half].double().cpu().numpy() - np.cos(phi)).max() <= 1.5 * 2.0 ** -23
+    # what the test is for: the same with the half turns rounded to fp32 fails by far
+    h = 2 * (phi / (2 * np.pi) - np.rint(phi / (2 * np.pi)))
+    assert np.abs(np.sin(np.pi * h.astype(np.float32).astype(np.float64)) - want).max() > 5 * 2.0 ** -28
