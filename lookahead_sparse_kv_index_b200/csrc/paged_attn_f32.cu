@@ -10,10 +10,13 @@
 // (cp.async); a lane works on two entries of a step at a time, and every group of LT lanes runs its own online softmax,
 // with a reference that moves only when a score passes it by 2^8.  The groups and warps meet at the end of a piece.
 //
-// Measured: 537 MB of rows under 4 query heads a kv head 115 us (4.7 TB/s, 72% of the copy rate), under 8 heads 186 us:
-// four products an element and head, so the fp32 pipe and HBM are near each other at 4 heads; 268 MB of heads of 64
-// elements 70 us (59%), of 32 elements 86 us (48%), by the work an entry costs whatever its length.  A batch of 17 MB with
-// a window takes 13 us, of which 9 are the two launches' own latencies.
+// Measured: 537 MB of rows under 1 to 4 query heads a kv head 116 us (4.6 TB/s, 71% of the copy rate), under 8 heads 185
+// us (45%).  No unit is full at 8 heads: the schedulers issue in 48% of the cycles, the fp32 pipe is busy in 27%, shared
+// memory in 45%; with 255 registers there are two warps a scheduler, which wait for shared memory and shuffles (0.7 of
+// 2.1 waiting cycles an instruction), for results (0.9) and for instructions (0.5), so the chain of an entry (its rows and
+// q from shared memory, products, shuffles, exponentials, products) is what the time goes to.  Heads of 64 elements: 121
+// us under 4 heads (69%), 183 under 8; of 32 elements 150 (56%) and 195, by the work an entry costs whatever its length.  A
+// batch of 17 MB with a window takes 13 us, of which 9 are the two launches' own latencies.
 #include <limits.h>
 
 #include "paged_attn.cuh"

@@ -30,7 +30,8 @@
 // that take turns (240 us) and weights in tensor memory in place of shared memory (224 us) were no faster; sixteen warps on
 // one tile took 226 us.
 // Under 8 heads or fewer a kv head the mma.sync kernel is faster (64 x 4096 entries: 84 us against 121), from 9 on, where
-// it would read the rows twice, this one (16 heads: 123 us against 133; 4 x 32768 entries 69 against 80).
+// it would read the rows twice, this one (16 heads: 123 us against 133; 4 x 32768 entries 69 against 80).  Between 9 and 64
+// heads HBM would allow 41 us there (64 x 4096) and 21 (4 x 32768): a tile costs what 128 heads cost, most rows of it empty.
 #include <cuda.h>
 
 #include "paged_attn.cuh"

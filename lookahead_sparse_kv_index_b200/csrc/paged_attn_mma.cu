@@ -30,10 +30,11 @@
 //
 // Measured: 2 x 65536 entries of 8 bf16 heads of 128 under 64 query heads, 537 MB, 96 us, 5.6 TB/s (86% of the copy rate);
 // 64 sequences of up to 16384 entries, 479 MB, 89 us (83%).  The same bytes of e4m3 rows, 118 us (72%): twice the elements
-// a byte, each converted, permuted and multiplied; 322 MB of ragged e4m3 contexts 75 us (66%).  Keeping the products'
-// range costs e4m3 rows 2 to 6% under up to 8 heads a kv head (two products and a maximum a weight), 9% under 16 and 18%
-// under 32, where registers spill (67 MB a head group of 8: 2 x 65536 entries of 128 under 16 heads 84 us, 2 x 32768
-// under 32 heads 104 us).
+// a byte, each converted, permuted and multiplied; 322 MB of ragged e4m3 contexts 75 us (66%).  More heads a kv head
+// cost e4m3 rows more work on the same bytes: 277 MB (2 x 65536 entries of 8 heads of 128) take 67 us under 8 heads a kv
+// head, 84 under 16 and 154 under 32, where the loop spills 480 bytes.  Keeping the products' range is two products and a
+// maximum a weight: 2 to 6% of the time under up to 8 heads, 9% under 16, 18% under 32.  Where 5% of the rows are zeros at
+// scale 1 among values of 0.01, most steps move a reference: 72 us in place of 66.
 #include <limits.h>
 
 #include "paged_attn.cuh"

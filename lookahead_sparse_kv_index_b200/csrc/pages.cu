@@ -5,7 +5,9 @@
 // forking are one CTA: it adds up what the call needs, counts free pages from index 0 until they suffice (nothing is
 // written before that), and lists them, round by round, for a thread each to hand to its row; 1024 threads take 16
 // counts each a round, so a pool of 64K pages is four rounds a pass.  Their latency is what they cost: a free, a fork of
-// 20 rows and its copies take 11 us.  The copy of whole pages is bound by HBM: 202 MB copied to other pages take 62 us,
+// 20 rows and its copies take 11 us.  New pages are looked for from the pool's front, which a pool in use holds: of pools
+// nine tenths held, 64 pages for as many rows take 7 us of 8,000 pages, 29 us of 100,000 and 206 us of a million; a call
+// that needs no page takes 6 to 8 us whatever the pool.  The copy of whole pages is bound by HBM: 202 MB copied to other pages take 62 us,
 // the copy rate.
 #include "paged.cuh"
 

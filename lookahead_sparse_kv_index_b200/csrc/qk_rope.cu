@@ -4,7 +4,7 @@
 // written to q_out / k_out and, with the values, to the slots of a paged cache.
 //
 // One pass: a row is read once and written once, so the call is bound by HBM for many tokens (16384 tokens of 48 bf16
-// heads of 128: 69 us, 5.8 TB/s, 90% of the copy rate) and by its latency for few.  A warp does rows of one token after
+// heads of 128: 70 us, 5.7 TB/s, 89% of the copy rate) and by its latency for few.  A warp does rows of one token after
 // the other, LPR lanes a row, and the device's warps share all rows evenly, whatever the number of tokens.  A lane owns
 // units of VP pairs of the row, i.e. VP elements of the rotated part's first half and the VP that pair with them (or whole
 // pairs of either half of the row where pairs are interleaved), so rotating needs no exchange between lanes, and both
