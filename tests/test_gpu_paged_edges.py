@@ -1,4 +1,4 @@
-"""Calls of lsa_paged_attn at the edges of what its description allows."""
+"""Calls of the paged-cache operators at the edges of what their descriptions allow."""
 import numpy as np
 import pytest
 import torch
@@ -70,3 +70,40 @@ def test_the_length_of_any_sequence_of_a_long_batch_is_reported(lsa, dtype, Hq, 
         assert err.item() == 3
         keep = torch.arange(B, device="cuda") != b
         assert torch.equal(out[keep].view(torch.uint8), want[keep].view(torch.uint8))
+
+
+@pytest.mark.parametrize("kind,Hq,Hkv,D,latent", [("f32", 4, 1, 256, False), ("bf16", 8, 2, 256, False),
+                                                 ("e4m3", 8, 2, 512, False), ("bf16", 16, 1, 512, True)])
+def test_append_copy_and_attention_past_32_bits(lsa, kind, Hq, Hkv, D, latent):
+    """The same calls over the last pages of a cache of 4.6 GB a tensor and over a small one: the same bits."""
+    page, n = 64, 3 * 64 + 17
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}[kind]
+    qt = torch.float32 if kind == "f32" else torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(23)
+    x = torch.randn((n, Hq + 2 * Hkv, D), generator=g, device="cuda").to(qt)
+    freq, _ = lsa.rope_frequencies(64)
+    rope = lsa.Rope(freq.cuda())
+    at = i32(range(n))
+    many = 4_600_000_000 // (page * Hkv * D * dt.itemsize)
+
+    def run(n_pages, use, to):
+        k = torch.zeros((n_pages, page, Hkv, D), dtype=dt, device="cuda")
+        v = None if latent else torch.zeros_like(k)
+        ks, vs = (torch.zeros((n_pages, page, Hkv), device="cuda") if kind == "e4m3" else None for _ in range(2))
+        cache = lsa.PageCache(k, v, ks, vs)
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        q = torch.empty((n, Hq, D), dtype=qt, device="cuda")
+        lsa.qk_norm_rope(x[:, :Hq], x[:, Hq:Hq + Hkv], None if latent else x[:, Hq + Hkv:], q_out=q, pos=at, rope=rope,
+                         cache=cache, table=i32([use]), seq=i32([0] * n), at=at, err=err)
+        lsa.page_copy(cache, i32(use), i32(to), err=err)
+        ws = torch.empty(lsa.paged_attn_workspace_size(cache, 2, Hq), dtype=torch.uint8, device="cuda")
+        out, lse = torch.empty((2, Hq, D), dtype=qt, device="cuda"), torch.empty((2, Hq), device="cuda")
+        lsa.paged_attn(q[-2:].contiguous(), cache, i32([use, to]), i32([n, n]), out, ws, lse=lse, err=err)
+        assert err.item() == 0
+        return out.clone(), lse.clone(), q
+
+    a = run(many, [many - 1, 3, many - 2, many - 9], [many - 4, many - 5, 0, many - 7])
+    b = run(9, [8, 3, 7, 1], [6, 5, 0, 2])
+    assert a[0].isfinite().all() and a[0].abs().amax(-1).min() > 0
+    for s, t in zip(a, b):
+        assert torch.equal(s, t)
