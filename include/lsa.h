@@ -458,7 +458,9 @@ lsa_status lsa_paged_attn(const void *Q, lsa_dtype q_dtype, int64_t q_stride, co
  *           written and *err = LSA_ERR_INVALID.
  * Cache types: that of `dtype`, or E4M3.  D a multiple of 16 up to 512; rot_dim
  * even, 0 .. D; pointers and strides 16-byte multiples.  Norms and rotations are
- * computed in fp32 and rounded once.  One launch; T = 0 launches nothing.
+ * computed in fp32 and rounded once (so sums of squares past fp32's range are infinite,
+ * and their head zero).  The entries that are written are no part of q, k or v (not
+ * checked).  One launch; T = 0 launches nothing.
  * ---------------------------------------------------------------------- */
 typedef struct lsa_rope {
     const double *freq;     /* device [rot_dim / 2] */
