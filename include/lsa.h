@@ -452,10 +452,9 @@ lsa_status lsa_paged_attn(const void *Q, lsa_dtype q_dtype, int64_t q_stride, co
  *           seq are not appended.  v is required unless the cache is latent (v ==
  *           k), where it must be NULL.  Rows of an E4M3 cache are rounded from
  *           fp32: scale = max|y| / 448 (at least 2^-126; 1 for a row of zeros), code =
- *           y / scale.  No two tokens
- *           may name the same entry.  An entry outside the table (n_rows rows,
- *           max_pages * page_size entries) or on a page outside [0, n_pages) is not
- *           written and *err = LSA_ERR_INVALID.
+ *           y / scale.  No two tokens may name the same entry.  An entry outside the
+ *           table (n_rows rows, max_pages * page_size entries) or on a page outside
+ *           [0, n_pages) is not written and *err = LSA_ERR_INVALID.
  * Cache types: that of `dtype`, or E4M3.  D a multiple of 16 up to 512; rot_dim
  * even, 0 .. D; pointers and strides 16-byte multiples.  Norms and rotations are
  * computed in fp32 and rounded once (so sums of squares past fp32's range are infinite,
